@@ -19,7 +19,9 @@ import torch
 __all__ = [
     "LIB_PATH", "lib", "MoEError", "Status", "LayerDesc", "quantize_int4", "quantize_fp8_rows", "rmsnorm",
     "route", "MoELayer", "DenseDesc", "DenseLayer", "FMT_INT4", "FMT_FP8", "PATH_AUTO", "PATH_DECODE",
-    "PATH_PREFILL", "noalloc_device_status", "set_wait_limit",
+    "PATH_PREFILL", "noalloc_device_status", "set_wait_limit", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
+    "linear", "linear_backward", "grouped_linear", "grouped_linear_backward", "swiglu", "swiglu_backward",
+    "linear_device_status",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "lib", "libmoe_int4.so")
@@ -119,6 +121,16 @@ def lib() -> ctypes.CDLL:
         L.moe_rmsnorm.restype = ctypes.c_int
         L.moe_ffn_device_status.argtypes = [vp, vp]
         L.moe_ffn_device_status.restype = ctypes.c_int
+        for name, args in {
+                "moe_linear_forward": [vp, i32, i32, vp, i32, vp, i32, vp, vp, vp, vp],
+                "moe_linear_backward": [vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, vp, vp, i32, vp],
+                "moe_grouped_linear_forward": [vp, i32, i32, vp, i32, i32, vp, vp, i32, vp],
+                "moe_grouped_linear_backward": [vp, vp, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp],
+                "moe_swiglu_forward": [vp, i32, i32, vp, vp],
+                "moe_swiglu_backward": [vp, vp, i32, i32, vp, vp],
+                "moe_linear_device_status": [vp]}.items():
+            getattr(L, name).argtypes = args
+            getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -430,3 +442,8 @@ class DenseLayer:
     def device_status(self, stream=None) -> int:
         """Synchronizes the stream; the device status of the last forward."""
         return lib().moe_ffn_device_status(_ptr(self.workspace), _stream(stream))
+
+
+from .linear_ops import (  # noqa: E402 - needs the names above
+    ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, grouped_linear, grouped_linear_backward, linear, linear_backward,
+    linear_device_status, swiglu, swiglu_backward)

@@ -1,0 +1,657 @@
+// bf16 matrix products for the linear and grouped linear operators, on the
+// 5th-generation tensor cores.
+//
+// One kernel computes, per matrix e (one expert, or the only matrix),
+//   LIN_FWD  y[r][n]  = sum_k x[r][k] W[n][k]     (then bias, activation, residual)
+//   LIN_DX   dx[r][k] = sum_n dy[r][n] W[n][k]
+//   LIN_DW   dw[n][k] = sum_r dy[r][n] x[r][k]
+// as D[lane][col] = sum_c A[lane][c] B[col][c]: the output feature that is
+// contiguous in memory is the lane (M = 128) and the output row the column
+// (up to 256), so a warp's stores run along rows of the output.  The
+// contracted index c is contiguous in memory for both operands of LIN_FWD and
+// for B of LIN_DX (K-major tiles); W of LIN_DX and both operands of LIN_DW
+// have it as their row index and are fed as MN-major tiles straight from the
+// same row-major matrices: no operand is transposed or copied beforehand.
+//
+// Tiles: 128 features x up to bn columns, steps of 64 along c, through a ring
+// of TMA-filled slots (A 16 KB, B bn x 128 B, 128-byte swizzle).  D is fp32 in
+// tensor memory, two accumulators, so a tile's epilogue overlaps the next
+// tile's MMAs.  TMA's zero fill pads c, features and rows at the tensors'
+// edges; what it cannot pad is the end of an expert's rows inside the tensor
+// when c runs over rows (LIN_DW): warp 2 zeroes those rows of both operands
+// in the slot before the MMAs read it, so rows of the next expert -- which may
+// hold NaN -- never enter.
+//
+// An expert's rows are cut into equal chunks of at most bn rows (rounded up to
+// 16), not into full chunks and a tail: a tail of a few rows would stream a
+// whole weight tile for them.  Each CTA derives the list from the offsets by a
+// scan over the (at most 256) experts.
+//
+// SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
+// shares one tile's contraction.  Each leaves its partial sums in its shared
+// memory, and the CTAs add each other's through distributed shared memory in
+// rank order: no scratch, no atomics, the same bits every time.
+//
+// Warps: 0 TMA producer, 1 MMA issuer, 2 row zeroing (LIN_DW), 3 tensor-memory
+// allocation, 4-7 epilogue.
+#include <cuda.h>
+
+#include <climits>
+
+#include "activation.cuh"
+#include "linear.cuh"
+#include "tcgen05.cuh"
+
+namespace moe {
+
+constexpr int LN_THREADS = 256;
+constexpr int LN_MAX_STAGES = 8;
+constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
+constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
+constexpr int LN_RING_BYTES = 196608;     // 4 slots of 48 KB, 6 of 32 KB or 8 of 24 KB
+constexpr int LN_TMEM_COLS = 512;
+static_assert(LN_RING_BYTES >= 256 * 128 * 4, "the partial sums of a split tile reuse the ring");
+
+// What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
+static __device__ int32_t g_linear_status;
+
+struct LinSmem {
+    uint64_t full[LN_MAX_STAGES];    // TMA data of the slot landed (tx counted)
+    uint64_t empty[LN_MAX_STAGES];   // the slot's MMAs completed (LIN_DW: and warp 2 is past it)
+    uint64_t fixed[LN_MAX_STAGES];   // warp 2 zeroed the slot's rows past the expert's end (ragged steps only)
+    uint64_t drained;                // all MMAs of this CTA completed
+    uint64_t acc_full[2];            // accumulator holds a finished tile
+    uint64_t acc_empty[2];           // epilogue finished reading the accumulator
+    uint32_t tmem_base;
+    int32_t status;                  // of this CTA; joined into g_linear_status at the end
+    int32_t first[LN_MAX_E + 1];     // chunks before each expert (LIN_FWD, LIN_DX)
+    int32_t begin[LN_MAX_E];         // the expert's rows
+    int32_t count[LN_MAX_E];
+    int32_t warp_sum[LN_THREADS / 32];
+};
+
+// Shared-memory matrix descriptor of an MN-major tile with the 128-byte
+// swizzle: rows of 64 values along M or N (128 bytes), one per c; 8 c are
+// 1024 bytes, the next 64 values along M or N one box of 64 c (8192 bytes)
+// further (leading byte offset).  16 c are 2048 bytes (+128 encoded).
+__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
+    return uint64_t((addr >> 4) & 0x3FFFu) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+struct Tile {
+    int e, fb;
+    int col0, ncols;      // output rows (LIN_FWD, LIN_DX: rows; LIN_DW: n) of the tile
+    int c0, k0, k1, clen; // contraction: first row (LIN_DW), steps [k0, k1), length
+};
+
+template <int MODE, bool SPLIT>
+__device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinParams& p, int n_units, int rank) {
+    // feature blocks in groups of 16, unit by unit within a group: about 148
+    // concurrent tiles then share 16 weight blocks and 9 row chunks in L2
+    const int gf = min(16, p.n_fblocks);
+    const int n_groups = (p.n_fblocks + gf - 1) / gf;
+    const int g = min(tile / (n_units * gf), n_groups - 1);
+    const int r = tile - g * n_units * gf;
+    const int gsize = min(gf, p.n_fblocks - g * gf);
+    const int unit = r / gsize;
+    Tile t;
+    t.fb = g * gf + r % gsize;
+    if (MODE == LIN_DW) {
+        const int ncb = (p.NC + p.bn - 1) / p.bn;
+        t.e = unit / ncb;
+        t.col0 = (unit - t.e * ncb) * p.bn;
+        t.ncols = min(p.bn, p.NC - t.col0);
+        t.c0 = sm->begin[t.e];
+        t.clen = sm->count[t.e];
+    } else {
+        int lo = 0, hi = p.E;              // the last expert whose first chunk is <= unit
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (sm->first[mid] <= unit) lo = mid; else hi = mid;
+        }
+        t.e = lo;
+        const int chunks = sm->first[lo + 1] - sm->first[lo], cnt = sm->count[lo];
+        const int size = ((cnt + chunks - 1) / chunks + 15) & ~15;
+        const int i = unit - sm->first[lo];
+        t.col0 = sm->begin[lo] + i * size;
+        t.ncols = max(0, min(size, cnt - i * size));
+        t.c0 = 0;
+        t.clen = p.C;
+    }
+    const int nk = (t.clen + 63) >> 6;
+    t.k0 = SPLIT ? int(int64_t(nk) * rank / p.split) : 0;
+    t.k1 = SPLIT ? int(int64_t(nk) * (rank + 1) / p.split) : nk;
+    return t;
+}
+
+// Two neighbouring features of one output row: bias, pre-activation,
+// activation, residual, rounding.  row: index into [rows, F] (or dw's rows).
+template <int MODE>
+__device__ __forceinline__ void finish_pair(const LinParams& p, int64_t idx, float a, float b, float bias_a,
+                                            float bias_b, uint32_t res) {
+    if (MODE == LIN_FWD) {
+        a += bias_a;
+        b += bias_b;
+        if (p.preact) *reinterpret_cast<uint32_t*>(p.preact + idx) = pack_bf16x2(a, b);
+        if (p.act != MOE_ACT_NONE) {
+            a = act_value(p.act, a);
+            b = act_value(p.act, b);
+        }
+        if (p.residual) {
+            a += bf16_lo(res);
+            b += bf16_hi(res);
+        }
+    }
+    if (p.out_fp32)
+        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + idx) = make_float2(a, b);
+    else
+        *reinterpret_cast<uint32_t*>(static_cast<bf16*>(p.out) + idx) = pack_bf16x2(a, b);
+}
+
+__device__ __forceinline__ float2 ld_dsmem_f32x2(const float* p, uint32_t rank) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    return v;
+}
+
+template <int MODE, bool SPLIT>
+__global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ CUtensorMap tm_a,
+                                                               const __grid_constant__ CUtensorMap tm_b, LinParams p) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* base = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    LinSmem* sm = reinterpret_cast<LinSmem*>(base + LN_RING_BYTES);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
+    const int stage_bytes = LN_A_BYTES + p.bn * 128;
+    uint32_t rank = 0;
+    if (SPLIT) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+
+    griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&tm_a);
+        prefetch_tmap(&tm_b);
+        for (int i = 0; i < LN_MAX_STAGES; ++i) {
+            mbar_init(&sm->full[i], 1);
+            mbar_init(&sm->empty[i], MODE == LIN_DW ? 2 : 1);
+            mbar_init(&sm->fixed[i], 1);
+        }
+        mbar_init(&sm->drained, 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&sm->acc_full[i], 1); mbar_init(&sm->acc_empty[i], 4); }
+        sm->status = DEV_OK;
+        fence_barrier_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(&sm->tmem_base, LN_TMEM_COLS);
+        tmem_relinquish();
+    }
+    griddep_wait();
+
+    // the row ranges, and for LIN_FWD / LIN_DX the chunks before each expert
+    int chunks = 0;
+    if (int(threadIdx.x) < p.E) {
+        int b = 0, c = p.rows;
+        if (p.offsets) {
+            b = p.offsets[threadIdx.x];
+            const int end = p.offsets[threadIdx.x + 1];
+            if (b >= 0 && end >= b && end <= p.rows) {
+                c = end - b;
+            } else {
+                b = c = 0;
+                if (blockIdx.x == 0) atomicOr(&g_linear_status, DEV_BAD_EXPERT);
+            }
+        }
+        sm->begin[threadIdx.x] = b;
+        sm->count[threadIdx.x] = c;
+        chunks = (c + p.bn - 1) / p.bn;
+    }
+    if (MODE != LIN_DW) {
+        int incl = chunks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sm->warp_sum[warp] = incl;
+        __syncthreads();
+        int before = 0;
+        for (int i = 0; i < warp; ++i) before += sm->warp_sum[i];
+        if (int(threadIdx.x) < p.E) {
+            sm->first[threadIdx.x + 1] = before + incl;
+            if (threadIdx.x == 0) sm->first[0] = 0;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm->tmem_base;
+    const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
+    const int n_tiles = n_units * p.n_fblocks;
+    const int tile0 = SPLIT ? int(blockIdx.x) / p.split : int(blockIdx.x);
+    const int tstep = SPLIT ? INT_MAX / 2 : int(gridDim.x);   // a split tile is its cluster's only one
+
+    if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            uint32_t slot = 0, par = 1, filled = 0;
+            bool ok = true;
+            for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
+                const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+                const int boxes = (t.ncols + 63) >> 6;
+                const uint32_t bytes = LN_A_BYTES + boxes * 8192;
+                for (int kk = t.k0; kk < t.k1; ++kk) {
+                    if (!mbar_wait(&sm->empty[slot], par, &sm->status)) { ok = false; break; }
+                    unsigned char* sa = base + slot * stage_bytes;
+                    unsigned char* sb = sa + LN_A_BYTES;
+                    uint64_t* bar = &sm->full[slot];
+                    mbar_arrive_expect_tx(bar, bytes);
+                    const int c = t.c0 + kk * 64;
+                    if (MODE == LIN_FWD) {
+                        tma_load_3d(sa, &tm_a, bar, c, t.fb * 128, t.e);
+                    } else if (MODE == LIN_DX) {
+                        tma_load_3d(sa, &tm_a, bar, t.fb * 128, c, t.e);
+                        tma_load_3d(sa + 8192, &tm_a, bar, t.fb * 128 + 64, c, t.e);
+                    } else {
+                        tma_load_2d(sa, &tm_a, bar, t.fb * 128, c);
+                        tma_load_2d(sa + 8192, &tm_a, bar, t.fb * 128 + 64, c);
+                    }
+                    for (int i = 0; i < boxes; ++i) {
+                        if (B_MN) tma_load_2d(sb + i * 8192, &tm_b, bar, t.col0 + i * 64, c);
+                        else tma_load_2d(sb + i * 8192, &tm_b, bar, c, t.col0 + i * 64);
+                    }
+                    ++filled;
+                    if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
+                }
+            }
+            // wind down: wait (bounded) for the loads still in flight to land
+            for (uint32_t i = 0; i < uint32_t(p.stages) && i < filled; ++i) {
+                const uint32_t j = filled - 1 - i;
+                mbar_wait(&sm->full[j % p.stages], (j / p.stages) & 1, nullptr);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (lane == 0) {
+            uint32_t slot = 0, par = 0, n = 0, fixpar = 0;   // fixpar: bit i, parity of slot i's next fix
+            bool ok = true;
+            for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
+                const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+                if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
+                const uint32_t idesc = tc_idesc_fmt(128, min(p.bn, (t.ncols + 15) & ~15), 1u) |
+                                       (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+                const uint32_t acc = n & 1;
+                if (!mbar_wait(&sm->acc_empty[acc], ((n >> 1) & 1) ^ 1, &sm->status)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t d_tmem = tmem + acc * 256;
+                for (int kk = t.k0; kk < t.k1; ++kk) {
+                    if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
+                    const int left = t.clen - kk * 64;
+                    if (MODE == LIN_DW && left < 64 && (left & 15)) {
+                        if (!mbar_wait(&sm->fixed[slot], (fixpar >> slot) & 1, &sm->status)) { ok = false; break; }
+                        fixpar ^= 1u << slot;
+                    }
+                    tc_fence_after();
+                    const unsigned char* sa = base + slot * stage_bytes;
+                    const uint64_t ad = A_MN ? sw128_desc_mn(smem_u32(sa)) : sw128_desc(sa);
+                    const uint64_t bd = B_MN ? sw128_desc_mn(smem_u32(sa + LN_A_BYTES)) : sw128_desc(sa + LN_A_BYTES);
+#pragma unroll
+                    for (int k16 = 0; k16 < 4; ++k16)
+                        if (k16 * 16 < left)
+                            umma<false>(d_tmem, ad + (A_MN ? 128 : 2) * k16, bd + (B_MN ? 128 : 2) * k16, idesc,
+                                        kk != t.k0 || k16 != 0);
+                    umma_commit(&sm->empty[slot]);
+                    if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
+                }
+                if (ok) umma_commit(&sm->acc_full[acc]);
+                ++n;
+            }
+            // wind down: wait (bounded) for the last MMAs
+            umma_commit(&sm->drained);
+            mbar_wait(&sm->drained, 0, nullptr);
+        }
+    } else if (warp == 2 && MODE == LIN_DW) {
+        // ---------------- zero the rows past the expert's end ----------------
+        // It takes every slot in turn, as the MMA issuer does: a parity wait
+        // is only meaningful for a waiter that is at most one use behind.
+        uint32_t slot = 0, par = 0;
+        bool ok = true;
+        for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
+            const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+            const int boxes = (t.ncols + 63) >> 6;
+            for (int kk = t.k0; kk < t.k1; ++kk) {
+                if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
+                const int left = t.clen - kk * 64;
+                const bool ragged = left < 64 && (left & 15);
+                if (ragged) {
+                    // a box is 64 rows of 128 bytes; the swizzle moves 16-byte
+                    // chunks within a row only.  The MMAs read up to the next
+                    // multiple of 16 rows.
+                    unsigned char* sa = base + slot * stage_bytes;
+                    const int chunks16 = ((16 - (left & 15)) * 128) / 16;
+                    for (int b = 0; b < 2 + boxes; ++b)
+                        for (int i = lane; i < chunks16; i += 32)
+                            st_shared_v4(sa + b * 8192 + left * 128 + i * 16, make_uint4(0, 0, 0, 0));
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (ragged) mbar_arrive(&sm->fixed[slot]);
+                    mbar_arrive(&sm->empty[slot]);
+                }
+                if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
+            }
+        }
+    } else if (warp >= 4) {
+        // ------------------------------ epilogue ------------------------------
+        const int ew = warp & 3;                 // TMEM lanes 32 ew .. 32 ew + 31
+        uint32_t n = 0;
+        for (int tile = tile0; tile < n_tiles; tile += tstep) {
+            const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+            const bool any = t.k0 < t.k1;
+            const uint32_t acc = n & 1;
+            if (any) {
+                if (!mbar_wait(&sm->acc_full[acc], (n >> 1) & 1, &sm->status)) break;
+                tc_fence_after();
+            }
+            const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
+            // features f, f + 1 of one column per lane: even lanes take the
+            // even column of each pair, odd lanes the odd one
+            const int f = t.fb * 128 + ew * 32 + (lane & ~1);
+            const bool fok = f < p.F;
+            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
+            uint32_t bias2 = 0;
+            if (MODE == LIN_FWD && p.bias && fok) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + f);
+            const float bias_a = bf16_lo(bias2), bias_b = bf16_hi(bias2);
+            for (int cc = 0; cc * 32 < t.ncols; ++cc) {
+                uint32_t v[32];
+                if (any) {
+                    tmem_ld32(taddr + cc * 32, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0u;
+                }
+                if (SPLIT) {   // partial sums [col][128], added up below
+                    float* red = reinterpret_cast<float*>(base) + cc * 32 * 128 + ew * 32 + lane;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) red[j * 128] = __uint_as_float(v[j]);
+                    continue;
+                }
+                uint32_t res[16];
+                if (MODE == LIN_FWD && p.residual) {
+#pragma unroll
+                    for (int jp = 0; jp < 16; ++jp) {   // all loads first: one latency per 32 columns
+                        const int col = cc * 32 + 2 * jp + (lane & 1);
+                        res[jp] = fok && col < t.ncols
+                                      ? *reinterpret_cast<const uint32_t*>(p.residual + (row0 + col) * p.F + f) : 0u;
+                    }
+                } else {
+#pragma unroll
+                    for (int jp = 0; jp < 16; ++jp) res[jp] = 0u;
+                }
+#pragma unroll
+                for (int jp = 0; jp < 16; ++jp) {
+                    const uint32_t a = v[2 * jp], b = v[2 * jp + 1];
+                    const uint32_t recv = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
+                    const int col = cc * 32 + 2 * jp + (lane & 1);
+                    if (fok && col < t.ncols)
+                        finish_pair<MODE>(p, (row0 + col) * p.F + f, __uint_as_float((lane & 1) ? recv : a),
+                                          __uint_as_float((lane & 1) ? b : recv), bias_a, bias_b, res[jp]);
+                }
+            }
+            if (any) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->acc_empty[acc]);
+                ++n;
+            }
+        }
+    }
+    if (SPLIT) {
+        __syncwarp();
+        cluster_sync();                          // every CTA's partial sums are in its shared memory
+        if (tile0 < n_tiles) {
+            const Tile t = get_tile<MODE, SPLIT>(tile0, sm, p, n_units, rank);
+            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
+            const float* red = reinterpret_cast<const float*>(base);
+            for (int i = int(rank) * LN_THREADS + int(threadIdx.x); i < t.ncols * 64; i += p.split * LN_THREADS) {
+                const int col = i >> 6, f = t.fb * 128 + 2 * (i & 63);
+                if (f >= p.F) continue;
+                const int64_t idx = (row0 + col) * p.F + f;
+                uint32_t bias2 = 0, res = 0;
+                if (MODE == LIN_FWD) {
+                    if (p.bias) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + f);
+                    if (p.residual) res = *reinterpret_cast<const uint32_t*>(p.residual + idx);
+                }
+                float a = 0.0f, b = 0.0f;
+                for (int s = 0; s < p.split; ++s) {
+                    const float2 v = ld_dsmem_f32x2(red + col * 128 + 2 * (i & 63), s);
+                    a += v.x;
+                    b += v.y;
+                }
+                finish_pair<MODE>(p, idx, a, b, bf16_lo(bias2), bf16_hi(bias2), res);
+            }
+        }
+        __syncwarp();
+        cluster_sync();                          // no CTA leaves while another reads its shared memory
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 3) {
+        tc_fence_after();
+        tmem_dealloc(tmem, LN_TMEM_COLS);
+    }
+    if (threadIdx.x == 0 && sm->status != DEV_OK) atomicOr(&g_linear_status, sm->status);
+}
+
+// ---------------------------------------------------------------------------
+// dz = dy * act'(z) and dbias = sum over the rows of dz (unrounded)
+//
+// HBM-bound: dy and z are read once, dz is written once, the column sums ride
+// along.  A cluster of AG_SPLIT CTAs takes a strip of 64 columns: 8 threads x
+// 16 bytes a row (one 128-byte line), 32 rows at a time, each CTA a part of
+// the rows.  A thread sums its rows in fp32, the CTA its 32 row lanes and the
+// cluster its CTAs in a fixed order.
+// ---------------------------------------------------------------------------
+constexpr int AG_THREADS = 256, AG_SPLIT = 8;
+
+template <bool DZ, bool DB>
+__global__ void __launch_bounds__(AG_THREADS) act_grad_kernel(const bf16* __restrict__ dy, const bf16* __restrict__ z,
+                                                              int T, int N, int act, bf16* __restrict__ dz,
+                                                              void* __restrict__ dbias, int dbias_fp32) {
+    __shared__ float part[32][65];
+    __shared__ float sums[64];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int split = blockIdx.x % AG_SPLIT, n0 = int(blockIdx.x / AG_SPLIT) * 64;
+    const int c8 = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    const int col = n0 + 8 * c8;
+    const int r0 = int(int64_t(T) * split / AG_SPLIT), r1 = int(int64_t(T) * (split + 1) / AG_SPLIT);
+    float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (col < N) {   // N is a multiple of 8
+#pragma unroll 4
+        for (int r = r0 + rl; r < r1; r += 32) {
+            const int64_t idx = int64_t(r) * N + col;
+            const uint4 d = *reinterpret_cast<const uint4*>(dy + idx);
+            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(dw[i]); v[2 * i + 1] = bf16_hi(dw[i]); }
+            if (DZ) {
+                const uint4 q = *reinterpret_cast<const uint4*>(z + idx);
+                const uint32_t zw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] *= act_slope(act, bf16_lo(zw[i]));
+                    v[2 * i + 1] *= act_slope(act, bf16_hi(zw[i]));
+                }
+                if (dz)
+                    *reinterpret_cast<uint4*>(dz + idx) =
+                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                                   pack_bf16x2(v[6], v[7]));
+            }
+            if (DB)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += v[i];
+        }
+    }
+    if (!DB) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) part[rl][8 * c8 + i] = s[i];
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        float t = 0.0f;
+        for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
+        sums[threadIdx.x] = t;
+    }
+    cluster_sync();
+    const int n = n0 + int(threadIdx.x);
+    if (split == 0 && threadIdx.x < 64 && n < N) {
+        float t = 0.0f;
+        for (int i = 0; i < AG_SPLIT; ++i) t += ld_dsmem_f32(&sums[threadIdx.x], i);
+        if (dbias_fp32) static_cast<float*>(dbias)[n] = t;
+        else static_cast<bf16*>(dbias)[n] = __float2bfloat16_rn(t);
+    }
+    cluster_sync();
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+namespace {
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(ptr);
+    }();
+    return fn;
+}
+
+// bf16 [mats, rows, inner] (mats = 0: 2-D [rows, inner]), boxes of 64 values x
+// box_rows rows with the 128-byte swizzle; reads past an edge give zeros.
+bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t rows, uint64_t mats, uint32_t box_rows) {
+    const EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {inner, rows, mats};
+    const cuuint64_t strides[2] = {inner * 2, inner * rows * 2};
+    const cuuint32_t box[3] = {64, box_rows, 1}, step[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, mats ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+moe_status sm_count(int* sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return MOE_OK;
+}
+
+template <typename... KArgs, typename... Args>
+moe_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                          cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
+}
+
+template <int MODE>
+moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int64_t tiles, int sms,
+                       cudaStream_t stream) {
+    const size_t smem = 1024 + LN_RING_BYTES + sizeof(LinSmem);
+    auto kernel = p.split > 1 ? linear_kernel<MODE, true> : linear_kernel<MODE, false>;
+    if (allow_max_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
+    const unsigned grid = p.split > 1 ? unsigned(tiles * p.split) : unsigned(tiles < sms ? tiles : sms);
+    return launch_cluster(kernel, grid, LN_THREADS, smem, unsigned(p.split), stream, ta, tb, p);
+}
+
+}  // namespace
+
+moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int32_t K, LinParams p,
+                         cudaStream_t stream) {
+    if (p.rows == 0) return MOE_OK;
+    int sms = 148;
+    if (sm_count(&sms) != MOE_OK) return MOE_ERR_CUDA;
+    p.F = mode == LIN_FWD ? N : K;
+    p.C = mode == LIN_FWD ? K : N;
+    p.NC = N;
+    p.n_fblocks = int(ceil_div(p.F, 128));
+    // columns of a tile: as many as an expert has rows on average (LIN_FWD,
+    // LIN_DX) or as there are (LIN_DW); few columns leave room for more slots
+    const int64_t cols = mode == LIN_DW ? N : ceil_div(p.rows, p.E);
+    p.bn = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    p.stages = LN_RING_BYTES / (LN_A_BYTES + p.bn * 128);
+    const int64_t units = mode == LIN_DW ? p.E * ceil_div(N, p.bn)
+                                         : p.rows / p.bn + (p.E < p.rows ? p.E : p.rows);   // at most
+    const int64_t tiles = (p.offsets || mode == LIN_DW ? units : ceil_div(p.rows, p.bn)) * p.n_fblocks;
+    const int64_t steps = ceil_div(mode == LIN_DW ? ceil_div(p.rows, p.E) : p.C, 64);
+    p.split = 1;
+    if (2 * tiles <= sms) {
+        int64_t s = sms / tiles;
+        if (s > 8) s = 8;
+        if (s > steps / 4) s = steps / 4;
+        if (s > 1) p.split = int(s);
+    }
+    CUtensorMap ta, tb;
+    const bool ok = mode == LIN_DW
+        ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
+        : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, 64);
+    if (!ok) return MOE_ERR_CUDA;
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, tiles, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, tiles, sms, stream);
+    return launch_mode<LIN_DW>(ta, tb, p, tiles, sms, stream);
+}
+
+moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
+                           int32_t dbias_fp32, cudaStream_t stream) {
+    const unsigned grid = unsigned(ceil_div(N, 64) * AG_SPLIT);
+    if (z && dbias)
+        return launch_cluster(act_grad_kernel<true, true>, grid, AG_THREADS, 0, AG_SPLIT, stream, dy, z, T, N, act, dz,
+                              dbias, dbias_fp32);
+    if (z)
+        return launch_cluster(act_grad_kernel<true, false>, grid, AG_THREADS, 0, AG_SPLIT, stream, dy, z, T, N, act,
+                              dz, dbias, dbias_fp32);
+    return launch_cluster(act_grad_kernel<false, true>, grid, AG_THREADS, 0, AG_SPLIT, stream, dy, z, T, N, act, dz,
+                          dbias, dbias_fp32);
+}
+
+moe_status set_wait_limit_linear(uint32_t cycles) {
+    return cuda_status(cudaMemcpyToSymbol(c_wait_limit, &cycles, sizeof(cycles)));
+}
+
+moe_status linear_device_status(cudaStream_t stream) {
+    int32_t v = 0;
+    const int32_t zero = 0;
+    if (cudaMemcpyFromSymbolAsync(&v, g_linear_status, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    if (v == DEV_OK) return MOE_OK;
+    if (cudaMemcpyToSymbolAsync(g_linear_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
+        cudaStreamSynchronize(stream) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return v & DEV_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_ERR_INVALID_ARG;
+}
+
+}  // namespace moe

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "ffn_decode.cuh"
+#include "linear.cuh"
 #include "tc_gemm.cuh"
 #include "norm.cuh"
 
@@ -804,7 +805,9 @@ extern "C" moe_status moe_set_wait_limit(int64_t cycles) {
     const uint32_t c = cycles > 0 && cycles < int64_t(kWaitCycles) ? uint32_t(cycles) : kWaitCycles;
     moe_status s = set_wait_limit_decode(c);
     if (s != MOE_OK) return s;
-    return set_wait_limit_tc(c);
+    s = set_wait_limit_tc(c);
+    if (s != MOE_OK) return s;
+    return set_wait_limit_linear(c);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,123 @@
+"""Refusals of the linear, grouped linear and SwiGLU entry points: what the C
+ABI and the Python functions reject before touching a device."""
+import os
+import re
+
+import pytest
+import torch
+
+import int4_quantized_expert_b200 as moe
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+S = moe.Status
+A = [(1 << 24) * (i + 1) for i in range(12)]   # aligned addresses far apart, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(moe.LIB_PATH):
+        from int4_quantized_expert_b200 import build
+        build.build()
+    return moe.lib()
+
+
+def test_exports_every_declared_symbol(lib):
+    src = open(os.path.join(ROOT, "include", "moe_linear.h")).read()
+    names = re.findall(r"MOE_API\s+[\w\s\*]+?\b(moe_\w+)\s*\(", src)
+    assert len(names) == 7
+    for n in names:
+        assert hasattr(lib, n), n
+
+
+def fwd(lib, **kw):
+    a = dict(x=A[0], T=4, K=16, w=A[1], N=24, bias=A[2], act=0, residual=A[3], preact=A[4], y=A[5])
+    a.update(kw)
+    return lib.moe_linear_forward(*a.values(), None)
+
+
+def test_linear_forward_refusals(lib):
+    for kw in (dict(T=-1), dict(T=(1 << 20) + 1), dict(K=0), dict(K=12), dict(K=65544), dict(N=4), dict(N=-8)):
+        assert fwd(lib, **kw) == S.UNSUPPORTED_SHAPE, kw
+    for kw in (dict(act=-1), dict(act=4), dict(x=None), dict(w=None), dict(y=None), dict(x=A[0] + 8), dict(bias=A[2] + 2),
+               dict(preact=A[4] + 4), dict(y=A[0]), dict(y=A[3] + 16), dict(preact=A[5]), dict(preact=A[2]),
+               dict(y=A[1] + 16)):
+        assert fwd(lib, **kw) == S.INVALID_ARG, kw
+    assert fwd(lib, T=0, x=None, w=None, y=None, bias=None, residual=None, preact=None) == S.OK
+
+
+def bwd(lib, **kw):
+    a = dict(dy=A[0], x=A[1], T=4, K=16, w=A[2], N=24, act=3, z=A[3], dz=A[4], dx=A[5], dw=A[6], db=A[7], dt=0)
+    a.update(kw)
+    return lib.moe_linear_backward(*a.values(), None)
+
+
+def test_linear_backward_refusals(lib):
+    for kw in (dict(T=-1), dict(K=20), dict(N=0)):
+        assert bwd(lib, **kw) == S.UNSUPPORTED_SHAPE, kw
+    for kw in (dict(act=9), dict(dt=2), dict(dy=None), dict(x=None), dict(w=None), dict(z=None), dict(dz=None),
+               dict(dx=A[0]), dict(dw=A[5]), dict(dz=A[0]), dict(db=A[6] + 32), dict(dw=A[6] + 8)):
+        assert bwd(lib, **kw) == S.INVALID_ARG, kw
+    # nothing wanted: nothing needed
+    assert bwd(lib, T=0, act=0, dy=None, x=None, w=None, z=None, dz=None, dx=None, dw=None, db=None) == S.OK
+
+
+def test_grouped_refusals(lib):
+    def f(**kw):
+        a = dict(x=A[0], n=4, K=16, w=A[1], E=3, N=24, off=A[2], y=A[3], dt=0)
+        a.update(kw)
+        return lib.moe_grouped_linear_forward(*a.values(), None)
+
+    def b(**kw):
+        a = dict(dy=A[0], x=A[1], n=4, K=16, w=A[2], E=3, N=24, off=A[3], dx=A[4], dw=A[5], dt=0)
+        a.update(kw)
+        return lib.moe_grouped_linear_backward(*a.values(), None)
+
+    for g in (f, b):
+        for kw in (dict(n=-1), dict(E=0), dict(E=257), dict(K=9), dict(N=65544)):
+            assert g(**kw) == S.UNSUPPORTED_SHAPE, kw
+        for kw in (dict(dt=3), dict(off=None), dict(x=None), dict(w=None), dict(off=A[3] + 4)):
+            assert g(**kw) == S.INVALID_ARG, kw
+    for kw in (dict(y=None), dict(y=A[0]), dict(y=A[2])):
+        assert f(**kw) == S.INVALID_ARG, kw
+    for kw in (dict(dy=None), dict(dx=A[0]), dict(dw=A[2]), dict(dx=A[5])):
+        assert b(**kw) == S.INVALID_ARG, kw
+    assert f(n=0, x=None, w=None, y=None) == S.OK
+    assert b(n=0, dy=None, x=None, w=None, dx=None, dw=None) == S.OK
+
+
+def test_swiglu_refusals(lib):
+    assert lib.moe_swiglu_forward(A[0], -1, 16, A[1], None) == S.UNSUPPORTED_SHAPE
+    assert lib.moe_swiglu_forward(A[0], 4, 12, A[1], None) == S.UNSUPPORTED_SHAPE
+    assert lib.moe_swiglu_forward(None, 4, 16, A[1], None) == S.INVALID_ARG
+    assert lib.moe_swiglu_forward(A[0], 4, 16, A[0], None) == S.INVALID_ARG
+    assert lib.moe_swiglu_forward(None, 0, 16, None, None) == S.OK
+    assert lib.moe_swiglu_backward(A[0], A[1], 4, 16, A[0], None) == S.INVALID_ARG
+    assert lib.moe_swiglu_backward(A[0], A[1] + 2, 4, 16, A[2], None) == S.INVALID_ARG
+    assert lib.moe_swiglu_backward(A[0], A[1], 4, 7, A[2], None) == S.UNSUPPORTED_SHAPE
+    assert lib.moe_swiglu_backward(None, None, 0, 8, None, None) == S.OK
+
+
+def test_python_refuses_what_it_cannot_marshal():
+    x, w = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(24, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.linear(x, w)
+    with pytest.raises(ValueError, match="2-D"):
+        moe.linear(x[0], w)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.linear_backward(x, x, w)
+    with pytest.raises(ValueError, match="3-D"):
+        moe.grouped_linear(_FakeCuda(x), w, None)
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.swiglu(x)
+
+
+class _FakeCuda:
+    """A 2-D tensor that says it is on a device: the next check is reached."""
+
+    def __init__(self, t):
+        self._t = t
+        self.is_cuda = True
+        self.shape = t.shape
+
+    def dim(self):
+        return self._t.dim()
