@@ -1,10 +1,22 @@
-// Activations and their derivatives in fp32 (linear.cu, swiglu.cu).
+// Activations and their derivatives in fp32, and bf16 pieces of rows (linear.cu, swiglu.cu).
 #pragma once
 
 #include "common.cuh"
 #include "moe_linear.h"
 
 namespace moe {
+
+// Eight bf16 values of a 16-byte piece of a row.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { f[2 * i] = bf16_lo(w[i]); f[2 * i + 1] = bf16_hi(w[i]); }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+}
 
 // 1 / (1 + exp(-z)) with the hardware exponential and division: a few ulps of
 // fp32.  For z below about -88 exp overflows to infinity and the result is 0.
@@ -30,14 +42,22 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
     return z < 0.0f ? half_erfc : 1.0f - half_erfc;
 }
 
-__device__ __forceinline__ float act_value(int act, float z) {
-    if (act == MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;   // keeps NaN
-    if (act == MOE_ACT_SILU) return z * sigmoid_fast(z);
-    if (act == MOE_ACT_GELU) {
-        float e;
-        return z * normal_cdf(z, e);
+// act of eight values.  The choice is made once for all of them, so the code
+// that is passed over is one jump away.
+__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // keeps NaN
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= sigmoid_fast(v[i]);
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float e;
+            v[i] *= normal_cdf(v[i], e);
+        }
     }
-    return z;
 }
 
 __device__ __forceinline__ float act_slope(int act, float z) {

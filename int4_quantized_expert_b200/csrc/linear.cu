@@ -50,6 +50,7 @@ constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
 constexpr int LN_RING_BYTES = 196608;     // 4 slots of 48 KB, 6 of 32 KB or 8 of 24 KB
 constexpr int LN_TMEM_COLS = 512;
+constexpr int LN_STG_PITCH = 36;          // floats; 4 mod 32, so 16-byte reads of neighbouring rows take distinct banks
 static_assert(LN_RING_BYTES >= 256 * 128 * 4, "the partial sums of a split tile reuse the ring");
 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
@@ -68,6 +69,7 @@ struct LinSmem {
     int32_t begin[LN_MAX_E];         // the expert's rows
     int32_t count[LN_MAX_E];
     int32_t warp_sum[LN_THREADS / 32];
+    alignas(16) float stage[4][32 * LN_STG_PITCH];   // epilogue warps: 32 columns x 32 features
 };
 
 // Shared-memory matrix descriptor of an MN-major tile with the 128-byte
@@ -124,35 +126,42 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
     return t;
 }
 
-// Two neighbouring features of one output row: bias, pre-activation,
-// activation, residual, rounding.  row: index into [rows, F] (or dw's rows).
+// Eight neighbouring features of one output row: bias, pre-activation,
+// activation, residual, rounding, store.  idx: of the first one in the output.
 template <int MODE>
-__device__ __forceinline__ void finish_pair(const LinParams& p, int64_t idx, float a, float b, float bias_a,
-                                            float bias_b, uint32_t res) {
+__device__ __forceinline__ void finish8(const LinParams& p, int64_t idx, float (&v)[8], const uint4& bias,
+                                        const uint4& res) {
     if (MODE == LIN_FWD) {
-        a += bias_a;
-        b += bias_b;
-        if (p.preact) *reinterpret_cast<uint32_t*>(p.preact + idx) = pack_bf16x2(a, b);
-        if (p.act != MOE_ACT_NONE) {
-            a = act_value(p.act, a);
-            b = act_value(p.act, b);
+        if (p.bias) {
+            float t[8];
+            unpack8(bias, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += t[i];
         }
+        if (p.preact) *reinterpret_cast<uint4*>(p.preact + idx) = pack8(v);
+        act_values(p.act, v);
         if (p.residual) {
-            a += bf16_lo(res);
-            b += bf16_hi(res);
+            float t[8];
+            unpack8(res, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += t[i];
         }
     }
-    if (p.out_fp32)
-        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + idx) = make_float2(a, b);
-    else
-        *reinterpret_cast<uint32_t*>(static_cast<bf16*>(p.out) + idx) = pack_bf16x2(a, b);
+    if (p.out_fp32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + idx);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(p.out) + idx) = pack8(v);
+    }
 }
 
-__device__ __forceinline__ float2 ld_dsmem_f32x2(const float* p, uint32_t rank) {
+__device__ __forceinline__ float4 ld_dsmem_f32x4(const float* p, uint32_t rank) {
     uint32_t remote;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(remote) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote) : "memory");
     return v;
 }
 
@@ -356,15 +365,24 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                 tc_fence_after();
             }
             const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
-            // features f, f + 1 of one column per lane: even lanes take the
-            // even column of each pair, odd lanes the odd one
-            const int f = t.fb * 128 + ew * 32 + (lane & ~1);
-            const bool fok = f < p.F;
+            // 32 columns at a time: a lane holds one feature of each, and gets
+            // eight features of one column (a 16-byte piece of an output row)
+            // back through the warp's staging buffer: rows 8 i + lane / 4
+            const int f = t.fb * 128 + ew * 32 + 8 * (lane & 3);
+            const bool fok = f < p.F;              // F is a multiple of 8
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
-            uint32_t bias2 = 0;
-            if (MODE == LIN_FWD && p.bias && fok) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + f);
-            const float bias_a = bf16_lo(bias2), bias_b = bf16_hi(bias2);
+            uint4 bias = make_uint4(0, 0, 0, 0);
+            if (MODE == LIN_FWD && p.bias && fok) bias = *reinterpret_cast<const uint4*>(p.bias + f);
+            float* stg = sm->stage[ew];
             for (int cc = 0; cc * 32 < t.ncols; ++cc) {
+                auto load_res = [&](int i) {
+                    const int col = cc * 32 + 8 * i + (lane >> 2);
+                    if (MODE == LIN_FWD && p.residual && i < 4 && fok && col < t.ncols)
+                        return *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
+                    return make_uint4(0, 0, 0, 0);
+                };
+                uint4 res = make_uint4(0, 0, 0, 0);
+                if (!SPLIT) res = load_res(0);
                 uint32_t v[32];
                 if (any) {
                     tmem_ld32(taddr + cc * 32, v);
@@ -378,27 +396,20 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     for (int j = 0; j < 32; ++j) red[j * 128] = __uint_as_float(v[j]);
                     continue;
                 }
-                uint32_t res[16];
-                if (MODE == LIN_FWD && p.residual) {
 #pragma unroll
-                    for (int jp = 0; jp < 16; ++jp) {   // all loads first: one latency per 32 columns
-                        const int col = cc * 32 + 2 * jp + (lane & 1);
-                        res[jp] = fok && col < t.ncols
-                                      ? *reinterpret_cast<const uint32_t*>(p.residual + (row0 + col) * p.F + f) : 0u;
-                    }
-                } else {
-#pragma unroll
-                    for (int jp = 0; jp < 16; ++jp) res[jp] = 0u;
+                for (int j = 0; j < 32; ++j) stg[j * LN_STG_PITCH + lane] = __uint_as_float(v[j]);
+                __syncwarp();
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 next = load_res(i + 1);
+                    const int r = 8 * i + (lane >> 2), col = cc * 32 + r;
+                    const float4* q = reinterpret_cast<const float4*>(stg + r * LN_STG_PITCH + 8 * (lane & 3));
+                    const float4 a = q[0], b = q[1];
+                    float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                    if (fok && col < t.ncols) finish8<MODE>(p, (row0 + col) * p.F + f, o, bias, res);
+                    res = next;
                 }
-#pragma unroll
-                for (int jp = 0; jp < 16; ++jp) {
-                    const uint32_t a = v[2 * jp], b = v[2 * jp + 1];
-                    const uint32_t recv = __shfl_xor_sync(0xffffffffu, (lane & 1) ? a : b, 1);
-                    const int col = cc * 32 + 2 * jp + (lane & 1);
-                    if (fok && col < t.ncols)
-                        finish_pair<MODE>(p, (row0 + col) * p.F + f, __uint_as_float((lane & 1) ? recv : a),
-                                          __uint_as_float((lane & 1) ? b : recv), bias_a, bias_b, res[jp]);
-                }
+                __syncwarp();
             }
             if (any) {
                 tc_fence_before();
@@ -415,22 +426,23 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
             const Tile t = get_tile<MODE, SPLIT>(tile0, sm, p, n_units, rank);
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             const float* red = reinterpret_cast<const float*>(base);
-            for (int i = int(rank) * LN_THREADS + int(threadIdx.x); i < t.ncols * 64; i += p.split * LN_THREADS) {
-                const int col = i >> 6, f = t.fb * 128 + 2 * (i & 63);
+            for (int i = int(rank) * LN_THREADS + int(threadIdx.x); i < t.ncols * 16; i += p.split * LN_THREADS) {
+                const int col = i >> 4, f = t.fb * 128 + 8 * (i & 15);
                 if (f >= p.F) continue;
                 const int64_t idx = (row0 + col) * p.F + f;
-                uint32_t bias2 = 0, res = 0;
+                uint4 bias = make_uint4(0, 0, 0, 0), res = bias;
                 if (MODE == LIN_FWD) {
-                    if (p.bias) bias2 = *reinterpret_cast<const uint32_t*>(p.bias + f);
-                    if (p.residual) res = *reinterpret_cast<const uint32_t*>(p.residual + idx);
+                    if (p.bias) bias = *reinterpret_cast<const uint4*>(p.bias + f);
+                    if (p.residual) res = *reinterpret_cast<const uint4*>(p.residual + idx);
                 }
-                float a = 0.0f, b = 0.0f;
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 for (int s = 0; s < p.split; ++s) {
-                    const float2 v = ld_dsmem_f32x2(red + col * 128 + 2 * (i & 63), s);
-                    a += v.x;
-                    b += v.y;
+                    const float4 a = ld_dsmem_f32x4(red + col * 128 + 8 * (i & 15), s);
+                    const float4 b = ld_dsmem_f32x4(red + col * 128 + 8 * (i & 15) + 4, s);
+                    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+                    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
                 }
-                finish_pair<MODE>(p, idx, a, b, bf16_lo(bias2), bf16_hi(bias2), res);
+                finish8<MODE>(p, idx, v, bias, res);
             }
         }
         __syncwarp();

@@ -10,17 +10,6 @@ namespace moe {
 
 constexpr int SG_THREADS = 256;
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { f[2 * i] = bf16_lo(w[i]); f[2 * i + 1] = bf16_hi(w[i]); }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
-}
-
 template <bool BACKWARD>
 __global__ void __launch_bounds__(SG_THREADS) swiglu_kernel(const bf16* __restrict__ gu, const bf16* __restrict__ dh,
                                                             int64_t n8, int F, bf16* __restrict__ out) {
