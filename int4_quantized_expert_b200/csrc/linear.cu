@@ -22,18 +22,29 @@
 // in the slot before the MMAs read it, so rows of the next expert -- which may
 // hold NaN -- never enter.
 //
+// LIN_PAIR: two CTAs of a cluster share a tile of 256 features x up to 256
+// columns.  Each loads its 128 features of A and its half of B's rows, and one
+// thread of the pair issues MMAs over both.  A CTA alone moves 48 KB into and
+// out of its shared memory for a step of 128 x 256 x 64, 768 cycles at 128
+// bytes a cycle, against 512 cycles of MMAs; a CTA of a pair moves 32 KB for
+// the same MMAs.
+//
 // An expert's rows are cut into equal chunks of at most bn rows (rounded up to
 // 16), not into full chunks and a tail: a tail of a few rows would stream a
 // whole weight tile for them.  Each CTA derives the list from the offsets by a
 // scan over the (at most 256) experts.
 //
-// SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
+// LIN_SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
 // shares one tile's contraction.  Each leaves its partial sums in its shared
 // memory, and the CTAs add each other's through distributed shared memory in
 // rank order: no scratch, no atomics, the same bits every time.
 //
-// Warps: 0 TMA producer, 1 MMA issuer, 2 row zeroing (LIN_DW), 3 tensor-memory
-// allocation, 4-7 epilogue.
+// Warps: 0 TMA producer, 1 MMA issuer, 2 slot hand-over (LIN_DW: zeroes rows;
+// LIN_PAIR: tells the MMA issuer's CTA that its own half has landed), 3
+// tensor-memory allocation, 4-11 epilogue.  The single threads of warps 0 and
+// 1 are picked by elect.sync: under `lane == 0` the TMA and MMA instructions'
+// uniform operands cost about 200 cycles each (708 cycles a step of three
+// loads against the MMAs' 512; 525 a step of both with elect.sync).
 #include <cuda.h>
 
 #include <climits>
@@ -44,7 +55,8 @@
 
 namespace moe {
 
-constexpr int LN_THREADS = 256;
+constexpr int LN_THREADS = 384;
+constexpr int LN_EPI_WARPS = 8;
 constexpr int LN_MAX_STAGES = 8;
 constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
@@ -56,21 +68,26 @@ static_assert(LN_RING_BYTES >= 256 * 128 * 4, "the partial sums of a split tile 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
 static __device__ int32_t g_linear_status;
 
+// How CTAs share tiles: one tile each, a cluster per tile along the
+// contraction, or two CTAs per tile of 256 features.
+enum LinShare { LIN_ONE, LIN_SPLIT, LIN_PAIR };
+
 struct LinSmem {
     uint64_t full[LN_MAX_STAGES];    // TMA data of the slot landed (tx counted)
-    uint64_t empty[LN_MAX_STAGES];   // the slot's MMAs completed (LIN_DW: and warp 2 is past it)
-    uint64_t fixed[LN_MAX_STAGES];   // warp 2 zeroed the slot's rows past the expert's end (ragged steps only)
-    uint64_t drained;                // all MMAs of this CTA completed
+    uint64_t empty[LN_MAX_STAGES];   // the slot's MMAs completed
+    uint64_t ready[LN_MAX_STAGES];   // LIN_DW, LIN_PAIR: warp 2 (of both CTAs) handed the slot over
+    uint64_t drained;                // all MMAs of this CTA (pair) completed
     uint64_t acc_full[2];            // accumulator holds a finished tile
-    uint64_t acc_empty[2];           // epilogue finished reading the accumulator
+    uint64_t acc_empty[2];           // epilogue (of both CTAs) finished reading the accumulator
     uint32_t tmem_base;
     int32_t status;                  // of this CTA; joined into g_linear_status at the end
     int32_t first[LN_MAX_E + 1];     // chunks before each expert (LIN_FWD, LIN_DX)
     int32_t begin[LN_MAX_E];         // the expert's rows
     int32_t count[LN_MAX_E];
     int32_t warp_sum[LN_THREADS / 32];
-    alignas(16) float stage[4][32 * LN_STG_PITCH];   // epilogue warps: 32 columns x 32 features
+    alignas(16) float stage[LN_EPI_WARPS][16 * LN_STG_PITCH];   // epilogue warps: 16 columns x 32 features
 };
+static_assert(1024 + LN_RING_BYTES + sizeof(LinSmem) <= 232448, "shared memory of a block");
 
 // Shared-memory matrix descriptor of an MN-major tile with the 128-byte
 // swizzle: rows of 64 values along M or N (128 bytes), one per c; 8 c are
@@ -81,23 +98,26 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
 }
 
 struct Tile {
-    int e, fb;
+    int e, f0;            // the CTA's first feature
     int col0, ncols;      // output rows (LIN_FWD, LIN_DX: rows; LIN_DW: n) of the tile
     int c0, k0, k1, clen; // contraction: first row (LIN_DW), steps [k0, k1), length
 };
 
-template <int MODE, bool SPLIT>
+template <int MODE, int SHARE>
 __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinParams& p, int n_units, int rank) {
-    // feature blocks in groups of 16, unit by unit within a group: about 148
-    // concurrent tiles then share 16 weight blocks and 9 row chunks in L2
-    const int gf = min(16, p.n_fblocks);
+    // feature blocks in groups of 2048 features, unit by unit within a group:
+    // the concurrent tiles of 148 CTAs then share 2048 features and 9 row
+    // chunks in L2
+    constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
+    const int gf = min(PAIR ? 8 : 16, p.n_fblocks);
     const int n_groups = (p.n_fblocks + gf - 1) / gf;
     const int g = min(tile / (n_units * gf), n_groups - 1);
     const int r = tile - g * n_units * gf;
     const int gsize = min(gf, p.n_fblocks - g * gf);
     const int unit = r / gsize;
     Tile t;
-    t.fb = g * gf + r % gsize;
+    const int fb = g * gf + (r - unit * gsize);
+    t.f0 = 128 * (PAIR ? 2 * fb + rank : fb);
     if (MODE == LIN_DW) {
         const int ncb = (p.NC + p.bn - 1) / p.bn;
         t.e = unit / ncb;
@@ -113,7 +133,8 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
         }
         t.e = lo;
         const int chunks = sm->first[lo + 1] - sm->first[lo], cnt = sm->count[lo];
-        const int size = ((cnt + chunks - 1) / chunks + 15) & ~15;
+        const int align = PAIR ? 31 : 15;   // of the MMA's N
+        const int size = ((cnt + chunks - 1) / chunks + align) & ~align;
         const int i = unit - sm->first[lo];
         t.col0 = sm->begin[lo] + i * size;
         t.ncols = max(0, min(size, cnt - i * size));
@@ -165,7 +186,7 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(const float* p, uint32_t rank) 
     return v;
 }
 
-template <int MODE, bool SPLIT>
+template <int MODE, int SHARE>
 __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ CUtensorMap tm_a,
                                                                const __grid_constant__ CUtensorMap tm_b, LinParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -174,9 +195,12 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     LinSmem* sm = reinterpret_cast<LinSmem*>(base + LN_RING_BYTES);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
-    const int stage_bytes = LN_A_BYTES + p.bn * 128;
+    constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
+    constexpr bool HAND_OVER = PAIR || MODE == LIN_DW;
+    const int stage_bytes = LN_A_BYTES + (PAIR ? p.bn / 2 : p.bn) * 128;
     uint32_t rank = 0;
-    if (SPLIT) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if (SHARE != LIN_ONE) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const bool leader = !PAIR || rank == 0;   // issues the MMAs
 
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
@@ -184,17 +208,20 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         prefetch_tmap(&tm_b);
         for (int i = 0; i < LN_MAX_STAGES; ++i) {
             mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], MODE == LIN_DW ? 2 : 1);
-            mbar_init(&sm->fixed[i], 1);
+            mbar_init(&sm->empty[i], 1);
+            mbar_init(&sm->ready[i], PAIR ? 2 : 1);
         }
         mbar_init(&sm->drained, 1);
-        for (int i = 0; i < 2; ++i) { mbar_init(&sm->acc_full[i], 1); mbar_init(&sm->acc_empty[i], 4); }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm->acc_full[i], 1);
+            mbar_init(&sm->acc_empty[i], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
+        }
         sm->status = DEV_OK;
         fence_barrier_init();
     }
     if (warp == 3) {
-        tmem_alloc(&sm->tmem_base, LN_TMEM_COLS);
-        tmem_relinquish();
+        tmem_alloc<PAIR>(&sm->tmem_base, LN_TMEM_COLS);
+        tmem_relinquish<PAIR>();
     }
     griddep_wait();
 
@@ -234,21 +261,27 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();   // the peer's barriers are initialized, both allocations done
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
     const int n_tiles = n_units * p.n_fblocks;
-    const int tile0 = SPLIT ? int(blockIdx.x) / p.split : int(blockIdx.x);
-    const int tstep = SPLIT ? INT_MAX / 2 : int(gridDim.x);   // a split tile is its cluster's only one
+    const int tile0 = SPLIT ? int(blockIdx.x) / p.split : PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
+    // a split tile is its cluster's only one
+    const int tstep = SPLIT ? INT_MAX / 2 : PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
+    // the MMA's N, and the rows of B (the columns of D) that this CTA loads
+    auto mma_n = [](const Tile& t) { return PAIR ? (t.ncols + 31) & ~31 : (t.ncols + 15) & ~15; };
+    auto b_first = [&](const Tile& t) { return PAIR ? int(rank) * (mma_n(t) / 2) : 0; };
+    auto b_boxes = [&](const Tile& t) { return ((PAIR ? mma_n(t) / 2 : t.ncols) + 63) >> 6; };
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t slot = 0, par = 1, filled = 0;
             bool ok = true;
             for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-                const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
-                const int boxes = (t.ncols + 63) >> 6;
+                const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+                const int boxes = b_boxes(t), row = t.col0 + b_first(t);
                 const uint32_t bytes = LN_A_BYTES + boxes * 8192;
                 for (int kk = t.k0; kk < t.k1; ++kk) {
                     if (!mbar_wait(&sm->empty[slot], par, &sm->status)) { ok = false; break; }
@@ -258,17 +291,17 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     mbar_arrive_expect_tx(bar, bytes);
                     const int c = t.c0 + kk * 64;
                     if (MODE == LIN_FWD) {
-                        tma_load_3d(sa, &tm_a, bar, c, t.fb * 128, t.e);
+                        tma_load_3d(sa, &tm_a, bar, c, t.f0, t.e);
                     } else if (MODE == LIN_DX) {
-                        tma_load_3d(sa, &tm_a, bar, t.fb * 128, c, t.e);
-                        tma_load_3d(sa + 8192, &tm_a, bar, t.fb * 128 + 64, c, t.e);
+                        tma_load_3d(sa, &tm_a, bar, t.f0, c, t.e);
+                        tma_load_3d(sa + 8192, &tm_a, bar, t.f0 + 64, c, t.e);
                     } else {
-                        tma_load_2d(sa, &tm_a, bar, t.fb * 128, c);
-                        tma_load_2d(sa + 8192, &tm_a, bar, t.fb * 128 + 64, c);
+                        tma_load_2d(sa, &tm_a, bar, t.f0, c);
+                        tma_load_2d(sa + 8192, &tm_a, bar, t.f0 + 64, c);
                     }
                     for (int i = 0; i < boxes; ++i) {
-                        if (B_MN) tma_load_2d(sb + i * 8192, &tm_b, bar, t.col0 + i * 64, c);
-                        else tma_load_2d(sb + i * 8192, &tm_b, bar, c, t.col0 + i * 64);
+                        if (B_MN) tma_load_2d(sb + i * 8192, &tm_b, bar, row + i * 64, c);
+                        else tma_load_2d(sb + i * 8192, &tm_b, bar, c, row + i * 64);
                     }
                     ++filled;
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
@@ -282,61 +315,65 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
-            uint32_t slot = 0, par = 0, n = 0, fixpar = 0;   // fixpar: bit i, parity of slot i's next fix
+        if (leader && elect_one()) {
+            uint32_t slot = 0, par = 0, n = 0;
             bool ok = true;
             for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-                const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+                const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
                 if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
-                const uint32_t idesc = tc_idesc_fmt(128, min(p.bn, (t.ncols + 15) & ~15), 1u) |
+                const uint32_t idesc = tc_idesc_fmt(PAIR ? 256 : 128, mma_n(t), 1u) |
                                        (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
                 const uint32_t acc = n & 1;
                 if (!mbar_wait(&sm->acc_empty[acc], ((n >> 1) & 1) ^ 1, &sm->status)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t d_tmem = tmem + acc * 256;
                 for (int kk = t.k0; kk < t.k1; ++kk) {
-                    if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
+                    if (!mbar_wait(HAND_OVER ? &sm->ready[slot] : &sm->full[slot], par, &sm->status)) { ok = false; break; }
                     const int left = t.clen - kk * 64;
-                    if (MODE == LIN_DW && left < 64 && (left & 15)) {
-                        if (!mbar_wait(&sm->fixed[slot], (fixpar >> slot) & 1, &sm->status)) { ok = false; break; }
-                        fixpar ^= 1u << slot;
-                    }
+                    // the peer's zeroes: this wait acquires at CTA scope only
+                    if (PAIR && MODE == LIN_DW && left < 64) asm volatile("fence.acq_rel.cluster;" ::: "memory");
                     tc_fence_after();
                     const unsigned char* sa = base + slot * stage_bytes;
                     const uint64_t ad = A_MN ? sw128_desc_mn(smem_u32(sa)) : sw128_desc(sa);
                     const uint64_t bd = B_MN ? sw128_desc_mn(smem_u32(sa + LN_A_BYTES)) : sw128_desc(sa + LN_A_BYTES);
 #pragma unroll
                     for (int k16 = 0; k16 < 4; ++k16)
-                        if (k16 * 16 < left)
-                            umma<false>(d_tmem, ad + (A_MN ? 128 : 2) * k16, bd + (B_MN ? 128 : 2) * k16, idesc,
-                                        kk != t.k0 || k16 != 0);
-                    umma_commit(&sm->empty[slot]);
+                        if (k16 * 16 < left) {
+                            const uint64_t a = ad + (A_MN ? 128 : 2) * k16, b = bd + (B_MN ? 128 : 2) * k16;
+                            const uint32_t accumulate = kk != t.k0 || k16 != 0;
+                            if (PAIR) umma_pair(d_tmem, a, b, idesc, accumulate);
+                            else umma<false>(d_tmem, a, b, idesc, accumulate);
+                        }
+                    if (PAIR) umma_commit_pair(&sm->empty[slot]);
+                    else umma_commit(&sm->empty[slot]);
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
                 }
-                if (ok) umma_commit(&sm->acc_full[acc]);
+                if (ok) {
+                    if (PAIR) umma_commit_pair(&sm->acc_full[acc]);
+                    else umma_commit(&sm->acc_full[acc]);
+                }
                 ++n;
             }
             // wind down: wait (bounded) for the last MMAs
-            umma_commit(&sm->drained);
+            if (PAIR) umma_commit_pair(&sm->drained);
+            else umma_commit(&sm->drained);
             mbar_wait(&sm->drained, 0, nullptr);
         }
-    } else if (warp == 2 && MODE == LIN_DW) {
-        // ---------------- zero the rows past the expert's end ----------------
-        // It takes every slot in turn, as the MMA issuer does: a parity wait
-        // is only meaningful for a waiter that is at most one use behind.
+    } else if (warp == 2 && HAND_OVER) {
+        // ---------------- hand the slots over to the MMA issuer ----------------
         uint32_t slot = 0, par = 0;
         bool ok = true;
         for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-            const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
-            const int boxes = (t.ncols + 63) >> 6;
+            const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+            const int boxes = b_boxes(t);
             for (int kk = t.k0; kk < t.k1; ++kk) {
                 if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
                 const int left = t.clen - kk * 64;
-                const bool ragged = left < 64 && (left & 15);
+                const bool ragged = MODE == LIN_DW && left < 64 && (left & 15);
                 if (ragged) {
-                    // a box is 64 rows of 128 bytes; the swizzle moves 16-byte
-                    // chunks within a row only.  The MMAs read up to the next
-                    // multiple of 16 rows.
+                    // zero the rows past the expert's end.  A box is 64 rows of
+                    // 128 bytes; the swizzle moves 16-byte chunks within a row
+                    // only.  The MMAs read up to the next multiple of 16 rows.
                     unsigned char* sa = base + slot * stage_bytes;
                     const int chunks16 = ((16 - (left & 15)) * 128) / 16;
                     for (int b = 0; b < 2 + boxes; ++b)
@@ -346,8 +383,9 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if (ragged) mbar_arrive(&sm->fixed[slot]);
-                    mbar_arrive(&sm->empty[slot]);
+                    if (PAIR && ragged) mbar_arrive_at<true>(&sm->ready[slot], 0);
+                    else if (PAIR) mbar_arrive_at(&sm->ready[slot], 0);
+                    else mbar_arrive(&sm->ready[slot]);
                 }
                 if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
             }
@@ -357,7 +395,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         const int ew = warp & 3;                 // TMEM lanes 32 ew .. 32 ew + 31
         uint32_t n = 0;
         for (int tile = tile0; tile < n_tiles; tile += tstep) {
-            const Tile t = get_tile<MODE, SPLIT>(tile, sm, p, n_units, rank);
+            const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
             const bool any = t.k0 < t.k1;
             const uint32_t acc = n & 1;
             if (any) {
@@ -365,24 +403,25 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                 tc_fence_after();
             }
             const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
-            // 32 columns at a time: a lane holds one feature of each, and gets
+            // 32 columns at a time, every other 32 for each of the two warps of
+            // these lanes.  A lane holds one feature of each column, and gets
             // eight features of one column (a 16-byte piece of an output row)
             // back through the warp's staging buffer: rows 8 i + lane / 4
-            const int f = t.fb * 128 + ew * 32 + 8 * (lane & 3);
+            const int f = t.f0 + ew * 32 + 8 * (lane & 3);
             const bool fok = f < p.F;              // F is a multiple of 8
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             uint4 bias = make_uint4(0, 0, 0, 0);
             if (MODE == LIN_FWD && p.bias && fok) bias = *reinterpret_cast<const uint4*>(p.bias + f);
-            float* stg = sm->stage[ew];
-            for (int cc = 0; cc * 32 < t.ncols; ++cc) {
-                auto load_res = [&](int i) {
+            float* stg = sm->stage[warp - 4];
+            for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
+                uint4 res[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
                     const int col = cc * 32 + 8 * i + (lane >> 2);
-                    if (MODE == LIN_FWD && p.residual && i < 4 && fok && col < t.ncols)
-                        return *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
-                    return make_uint4(0, 0, 0, 0);
-                };
-                uint4 res = make_uint4(0, 0, 0, 0);
-                if (!SPLIT) res = load_res(0);
+                    res[i] = make_uint4(0, 0, 0, 0);
+                    if (MODE == LIN_FWD && !SPLIT && p.residual && fok && col < t.ncols)
+                        res[i] = *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
+                }
                 uint32_t v[32];
                 if (any) {
                     tmem_ld32(taddr + cc * 32, v);
@@ -397,24 +436,35 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     continue;
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) stg[j * LN_STG_PITCH + lane] = __uint_as_float(v[j]);
-                __syncwarp();
-#pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 next = load_res(i + 1);
-                    const int r = 8 * i + (lane >> 2), col = cc * 32 + r;
-                    const float4* q = reinterpret_cast<const float4*>(stg + r * LN_STG_PITCH + 8 * (lane & 3));
-                    const float4 a = q[0], b = q[1];
-                    float o[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-                    if (fok && col < t.ncols) finish8<MODE>(p, (row0 + col) * p.F + f, o, bias, res);
-                    res = next;
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) stg[j * LN_STG_PITCH + lane] = __uint_as_float(v[16 * h + j]);
+                    __syncwarp();
+                    float4 q[2][2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4* s = reinterpret_cast<const float4*>(stg + (8 * i + (lane >> 2)) * LN_STG_PITCH +
+                                                                          8 * (lane & 3));
+                        q[i][0] = s[0];
+                        q[i][1] = s[1];
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int col = cc * 32 + 16 * h + 8 * i + (lane >> 2);
+                        float o[8] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w,
+                                      q[i][1].x, q[i][1].y, q[i][1].z, q[i][1].w};
+                        if (fok && col < t.ncols) finish8<MODE>(p, (row0 + col) * p.F + f, o, bias, res[2 * h + i]);
+                    }
                 }
-                __syncwarp();
             }
             if (any) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm->acc_empty[acc]);
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_at(&sm->acc_empty[acc], 0);
+                    else mbar_arrive(&sm->acc_empty[acc]);
+                }
                 ++n;
             }
         }
@@ -423,11 +473,11 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         __syncwarp();
         cluster_sync();                          // every CTA's partial sums are in its shared memory
         if (tile0 < n_tiles) {
-            const Tile t = get_tile<MODE, SPLIT>(tile0, sm, p, n_units, rank);
+            const Tile t = get_tile<MODE, SHARE>(tile0, sm, p, n_units, rank);
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             const float* red = reinterpret_cast<const float*>(base);
             for (int i = int(rank) * LN_THREADS + int(threadIdx.x); i < t.ncols * 16; i += p.split * LN_THREADS) {
-                const int col = i >> 4, f = t.fb * 128 + 8 * (i & 15);
+                const int col = i >> 4, f = t.f0 + 8 * (i & 15);
                 if (f >= p.F) continue;
                 const int64_t idx = (row0 + col) * p.F + f;
                 uint4 bias = make_uint4(0, 0, 0, 0), res = bias;
@@ -448,11 +498,17 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         __syncwarp();
         cluster_sync();                          // no CTA leaves while another reads its shared memory
     }
+    if (PAIR) {
+        __syncwarp();
+        cluster_sync();                          // the pair's MMAs and remote arrivals are over
+        // ... and the last commit, which arrives in both CTAs, has arrived here
+        if (threadIdx.x == 32) mbar_wait(&sm->drained, 0, nullptr);
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc(tmem, LN_TMEM_COLS);
+        tmem_dealloc<PAIR>(tmem, LN_TMEM_COLS);
     }
     if (threadIdx.x == 0 && sm->status != DEV_OK) atomicOr(&g_linear_status, sm->status);
 }
@@ -590,13 +646,15 @@ moe_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned bloc
 }
 
 template <int MODE>
-moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int64_t tiles, int sms,
-                       cudaStream_t stream) {
+moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, bool pair, int64_t tiles,
+                       int sms, cudaStream_t stream) {
     const size_t smem = 1024 + LN_RING_BYTES + sizeof(LinSmem);
-    auto kernel = p.split > 1 ? linear_kernel<MODE, true> : linear_kernel<MODE, false>;
+    auto kernel = pair          ? linear_kernel<MODE, LIN_PAIR>
+                  : p.split > 1 ? linear_kernel<MODE, LIN_SPLIT>
+                                : linear_kernel<MODE, LIN_ONE>;
     if (allow_max_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
-    const unsigned grid = p.split > 1 ? unsigned(tiles * p.split) : unsigned(tiles < sms ? tiles : sms);
-    return launch_cluster(kernel, grid, LN_THREADS, smem, unsigned(p.split), stream, ta, tb, p);
+    const int64_t cluster = pair ? 2 : p.split, grid = p.split > 1 ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
+    return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, smem, unsigned(cluster), stream, ta, tb, p);
 }
 
 }  // namespace
@@ -609,18 +667,22 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
     p.F = mode == LIN_FWD ? N : K;
     p.C = mode == LIN_FWD ? K : N;
     p.NC = N;
-    p.n_fblocks = int(ceil_div(p.F, 128));
     // columns of a tile: as many as an expert has rows on average (LIN_FWD,
     // LIN_DX) or as there are (LIN_DW); few columns leave room for more slots
     const int64_t cols = mode == LIN_DW ? N : ceil_div(p.rows, p.E);
     p.bn = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
-    p.stages = LN_RING_BYTES / (LN_A_BYTES + p.bn * 128);
     const int64_t units = mode == LIN_DW ? p.E * ceil_div(N, p.bn)
-                                         : p.rows / p.bn + (p.E < p.rows ? p.E : p.rows);   // at most
-    const int64_t tiles = (p.offsets || mode == LIN_DW ? units : ceil_div(p.rows, p.bn)) * p.n_fblocks;
+                          : p.offsets    ? p.rows / p.bn + (p.E < p.rows ? p.E : p.rows)   // at most
+                                         : ceil_div(p.rows, p.bn);
+    // wide tiles go to pairs of CTAs, unless there are so few that more than
+    // half of the pairs had none
+    const bool pair = p.bn == 256 && 2 * units * ceil_div(p.F, 256) > sms / 2;
+    p.stages = LN_RING_BYTES / (LN_A_BYTES + (pair ? p.bn / 2 : p.bn) * 128);
+    p.n_fblocks = int(ceil_div(p.F, pair ? 256 : 128));
+    const int64_t tiles = units * p.n_fblocks;
     const int64_t steps = ceil_div(mode == LIN_DW ? ceil_div(p.rows, p.E) : p.C, 64);
     p.split = 1;
-    if (2 * tiles <= sms) {
+    if (!pair && 2 * tiles <= sms) {
         int64_t s = sms / tiles;
         if (s > 8) s = 8;
         if (s > steps / 4) s = steps / 4;
@@ -631,9 +693,9 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
         ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
         : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, 64);
     if (!ok) return MOE_ERR_CUDA;
-    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, tiles, sms, stream);
-    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, tiles, sms, stream);
-    return launch_mode<LIN_DW>(ta, tb, p, tiles, sms, stream);
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, pair, tiles, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, pair, tiles, sms, stream);
+    return launch_mode<LIN_DW>(ta, tb, p, pair, tiles, sms, stream);
 }
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
