@@ -42,18 +42,19 @@ __device__ __forceinline__ float normal_cdf(float z, float& e) {
     return z < 0.0f ? half_erfc : 1.0f - half_erfc;
 }
 
-// act of eight values.  The choice is made once for all of them, so the code
-// that is passed over is one jump away.
-__device__ __forceinline__ void act_values(int act, float (&v)[8]) {
+// act of N values.  The choice is made once for all of them, so the code that
+// is passed over is one jump away.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
     if (act == MOE_ACT_RELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // keeps NaN
+        for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];   // keeps NaN
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= sigmoid_fast(v[i]);
+        for (int i = 0; i < N; ++i) v[i] *= sigmoid_fast(v[i]);
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < N; ++i) {
             float e;
             v[i] *= normal_cdf(v[i], e);
         }

@@ -62,7 +62,7 @@ constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
 constexpr int LN_RING_BYTES = 196608;     // 4 slots of 48 KB, 6 of 32 KB or 8 of 24 KB
 constexpr int LN_TMEM_COLS = 512;
-constexpr int LN_STG_PITCH = 36;          // floats; 4 mod 32, so 16-byte reads of neighbouring rows take distinct banks
+constexpr int LN_STG_BYTES = 32 * 64;     // an epilogue warp's staging buffer: 32 columns x 32 features, bf16
 static_assert(LN_RING_BYTES >= 256 * 128 * 4, "the partial sums of a split tile reuse the ring");
 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
@@ -85,7 +85,7 @@ struct LinSmem {
     int32_t begin[LN_MAX_E];         // the expert's rows
     int32_t count[LN_MAX_E];
     int32_t warp_sum[LN_THREADS / 32];
-    alignas(16) float stage[LN_EPI_WARPS][16 * LN_STG_PITCH];   // epilogue warps: 16 columns x 32 features
+    alignas(128) unsigned char stage[LN_EPI_WARPS][LN_STG_BYTES];
 };
 static_assert(1024 + LN_RING_BYTES + sizeof(LinSmem) <= 232448, "shared memory of a block");
 
@@ -147,7 +147,7 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
     return t;
 }
 
-// Eight neighbouring features of one output row: bias, pre-activation,
+// Eight neighbouring features of one output row (LIN_SPLIT): bias, pre-activation,
 // activation, residual, rounding, store.  idx: of the first one in the output.
 template <int MODE>
 __device__ __forceinline__ void finish8(const LinParams& p, int64_t idx, float (&v)[8], const uint4& bias,
@@ -175,6 +175,108 @@ __device__ __forceinline__ void finish8(const LinParams& p, int64_t idx, float (
     } else {
         *reinterpret_cast<uint4*>(static_cast<bf16*>(p.out) + idx) = pack8(v);
     }
+}
+
+// 32 lanes x 32 columns of an accumulator as fragments (tmem_ld_frag): v[h] has
+// the lanes 16 h .. 16 h + 15.
+__device__ __forceinline__ void tmem_ld_block(uint32_t taddr, uint32_t (&v)[2][16]) {
+    tmem_ld_frag(taddr, v[0]);
+    tmem_ld_frag(taddr + (16u << 16), v[1]);
+}
+
+// The same of a block of 32 features (from f0) x up to ncols columns, output
+// rows row .., held as fragments.  Rows of the output are stored and rows of
+// the residual loaded as 16-byte pieces, four lanes to a row; between these and
+// the fragments they are transposed by stmatrix / ldmatrix through the warp's
+// staging buffer of 64-byte rows (piece q of row r at q ^ (r / 2 % 4): the eight
+// rows of a matrix, and the two rows that eight lanes read, take distinct
+// banks).  Against 4-byte shared-memory stores of the fp32 values and 32-byte
+// loads this is a third of the shared-memory traffic.
+template <int MODE>
+__device__ __forceinline__ void finish_block(const LinParams& p, float (&a)[2][16], int64_t row, int ncols, int f0,
+                                             uint32_t stage, int lane) {
+    const int f = f0 + 8 * (lane & 3);          // this lane's piece of rows 8 i + lane / 4
+    const int rl = lane >> 2;
+    const bool fok = f < p.F;                   // F is a multiple of 8
+    const uint32_t piece = stage + rl * 64 + (((lane & 3) ^ ((lane >> 3) & 3)) << 4);                // + 512 i
+    const uint32_t mat = stage + (lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4);         // + 512 i
+    // two columns of one feature in a register: what row t / 4 (+ 8 b + 16 h) of
+    // the fragments has at columns 8 i + 2 (t % 4) and + 1
+    auto store_rows = [&](bf16* out) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t m[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                m[q] = pack_bf16x2(a[q >> 1][4 * i + 2 * (q & 1)], a[q >> 1][4 * i + 2 * (q & 1) + 1]);
+            st_matrix4_t(mat + 512 * i, m);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint4 v = ld_shared_v4_at(piece + 512 * i);
+            if (fok && 8 * i + rl < ncols) *reinterpret_cast<uint4*>(out + (row + 8 * i + rl) * p.F + f) = v;
+        }
+        __syncwarp();
+    };
+    uint4 res[4];
+    if (MODE == LIN_FWD) {
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                res[i] = make_uint4(0, 0, 0, 0);
+                if (fok && 8 * i + rl < ncols)
+                    res[i] = *reinterpret_cast<const uint4*>(p.residual + (row + 8 * i + rl) * p.F + f);
+            }
+        }
+        if (p.bias) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int fq = f0 + 8 * q + rl;
+                const float b = fq < p.F ? __bfloat162float(p.bias[fq]) : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[q >> 1][4 * i + 2 * (q & 1)] += b;
+                    a[q >> 1][4 * i + 2 * (q & 1) + 1] += b;
+                }
+            }
+        }
+        if (p.preact) store_rows(p.preact);
+        act_values(p.act, a[0]);
+        act_values(p.act, a[1]);
+        if (p.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_shared_v4_at(piece + 512 * i, res[i]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t m[4];
+                ld_matrix4_t(mat + 512 * i, m);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    a[q >> 1][4 * i + 2 * (q & 1)] += bf16_lo(m[q]);
+                    a[q >> 1][4 * i + 2 * (q & 1) + 1] += bf16_hi(m[q]);
+                }
+            }
+            __syncwarp();
+        }
+    }
+    if (!p.out_fp32) {
+        store_rows(static_cast<bf16*>(p.out));
+        return;
+    }
+    // eight lanes hold the 32 bytes of eight features of a column
+    float* out = static_cast<float*>(p.out) + row * p.F + f0 + rl;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = 8 * i + 2 * (lane & 3) + j;
+                if (f0 + 8 * q < p.F && c < ncols)
+                    out[int64_t(c) * p.F + 8 * q] = a[q >> 1][4 * i + 2 * (q & 1) + j];
+            }
 }
 
 __device__ __forceinline__ float4 ld_dsmem_f32x4(const float* p, uint32_t rank) {
@@ -403,70 +505,51 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                 tc_fence_after();
             }
             const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
-            // 32 columns at a time, every other 32 for each of the two warps of
-            // these lanes.  A lane holds one feature of each column, and gets
-            // eight features of one column (a 16-byte piece of an output row)
-            // back through the warp's staging buffer: rows 8 i + lane / 4
-            const int f = t.f0 + ew * 32 + 8 * (lane & 3);
-            const bool fok = f < p.F;              // F is a multiple of 8
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
-            uint4 bias = make_uint4(0, 0, 0, 0);
-            if (MODE == LIN_FWD && p.bias && fok) bias = *reinterpret_cast<const uint4*>(p.bias + f);
-            float* stg = sm->stage[warp - 4];
-            for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
-                uint4 res[4];
+            if (SPLIT) {   // partial sums [col][128], added up below
+                for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
+                    uint32_t v[32];
+                    if (any) {
+                        tmem_ld32(taddr + cc * 32, v);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = cc * 32 + 8 * i + (lane >> 2);
-                    res[i] = make_uint4(0, 0, 0, 0);
-                    if (MODE == LIN_FWD && !SPLIT && p.residual && fok && col < t.ncols)
-                        res[i] = *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
-                }
-                uint32_t v[32];
-                if (any) {
-                    tmem_ld32(taddr + cc * 32, v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0u;
-                }
-                if (SPLIT) {   // partial sums [col][128], added up below
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
                     float* red = reinterpret_cast<float*>(base) + cc * 32 * 128 + ew * 32 + lane;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) red[j * 128] = __uint_as_float(v[j]);
-                    continue;
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) stg[j * LN_STG_PITCH + lane] = __uint_as_float(v[16 * h + j]);
+            } else {
+                // every other 32 columns for each of the two warps of these lanes
+                auto release = [&] {
+                    tc_fence_before();
                     __syncwarp();
-                    float4 q[2][2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4* s = reinterpret_cast<const float4*>(stg + (8 * i + (lane >> 2)) * LN_STG_PITCH +
-                                                                          8 * (lane & 3));
-                        q[i][0] = s[0];
-                        q[i][1] = s[1];
+                    if (any && lane == 0) {
+                        if (PAIR) mbar_arrive_at(&sm->acc_empty[acc], 0);
+                        else mbar_arrive(&sm->acc_empty[acc]);
                     }
-                    __syncwarp();
+                };
+                const int nb = (t.ncols + 31) >> 5;
+                int cc = (warp - 4) >> 2;
+                uint32_t v[2][16];
+                if (cc >= nb) release();
+                else if (any) tmem_ld_block(taddr + cc * 32, v);
+                for (; cc < nb; cc += 2) {
+                    float a[2][16];
+                    if (any) tmem_wait_ld(v);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int col = cc * 32 + 16 * h + 8 * i + (lane >> 2);
-                        float o[8] = {q[i][0].x, q[i][0].y, q[i][0].z, q[i][0].w,
-                                      q[i][1].x, q[i][1].y, q[i][1].z, q[i][1].w};
-                        if (fok && col < t.ncols) finish8<MODE>(p, (row0 + col) * p.F + f, o, bias, res[2 * h + i]);
-                    }
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) a[h][j] = any ? __uint_as_float(v[h][j]) : 0.0f;
+                    // the next block's load runs under this block's arithmetic and
+                    // stores; after the last one the accumulator is free
+                    if (cc + 2 >= nb) release();
+                    else if (any) tmem_ld_block(taddr + cc * 32 + 64, v);
+                    finish_block<MODE>(p, a, row0 + cc * 32, t.ncols - cc * 32, t.f0 + ew * 32,
+                                       smem_u32(sm->stage[warp - 4]), lane);
                 }
             }
-            if (any) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_at(&sm->acc_empty[acc], 0);
-                    else mbar_arrive(&sm->acc_empty[acc]);
-                }
-                ++n;
-            }
+            if (any) ++n;
         }
     }
     if (SPLIT) {
