@@ -18,28 +18,76 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// 1 / (1 + exp(-z)) with the hardware exponential and division: a few ulps of
-// fp32.  For z below about -88 exp overflows to infinity and the result is 0.
-__device__ __forceinline__ float sigmoid_fast(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// 2^x, 1 / x: the hardware's approximations (relative errors 2^-22 and 2^-23),
+// results below 2^-126 flushed to 0, without the instructions that would keep them.
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2), from which
-// the density is e / sqrt(2 pi).  With x = |z| / sqrt(2),
+// two fp32 values at a time
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 1 / (1 + exp(-z)): a few ulps of fp32.  For z below about -88 the power of two
+// is infinite and the result 0.
+__device__ __forceinline__ float sigmoid_fast(float z) { return rcp_ftz(1.0f + ex2_ftz(-1.44269504f * z)); }
+
+// h = erfc(|z| / sqrt(2)) / 2, the normal distribution function at -|z|, and
+// e = exp(-z^2 / 2), from which the density is e / sqrt(2 pi).  With x = |z| / sqrt(2),
 //   erfc(x) = (a1 t + a2 t^2 + a3 t^3 + a4 t^4 + a5 t^5) exp(-x^2),  t = 1 / (1 + p x)
 // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26: absolute
-// error below 1.5e-7), and Phi = erfc(x) / 2 for z < 0, 1 - erfc(x) / 2 above.
-// CUDA's erff costs about three times the instructions, which a tile's
-// epilogue does not hide at short contraction lengths; the error here is far
-// below the bf16 step the result is rounded to.
-__device__ __forceinline__ float normal_cdf(float z, float& e) {
-    const float x = fabsf(z) * 0.70710678f;
-    e = __expf(-0.5f * z * z);
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float half_erfc = 0.5f * q * t * e;
-    return z < 0.0f ? half_erfc : 1.0f - half_erfc;
+// error below 1.5e-7), far below the bf16 step the result is rounded to.  An
+// epilogue's 128 x 256 values take 10 instructions each this way (two of them
+// on the quarter-rate unit); scalar and with denormals kept it was 28, and a
+// tile's epilogue (15.8k cycles) outlasted the MMAs of a contraction of 1416.
+__device__ __forceinline__ void normal_tail(float2 z, float2& h, float2& e) {
+    const float2 az = make_float2(fabsf(z.x), fabsf(z.y));
+    const float2 w = mul2(mul2(z, z), both(-0.72134752f));
+    e = make_float2(ex2_ftz(w.x), ex2_ftz(w.y));
+    const float2 d = fma2(az, both(0.3275911f * 0.70710678f), both(1.0f));
+    const float2 t = make_float2(rcp_ftz(d.x), rcp_ftz(d.y));
+    float2 q = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+    q = fma2(q, t, both(0.5f * 1.421413741f));
+    q = fma2(q, t, both(0.5f * -0.284496736f));
+    q = fma2(q, t, both(0.5f * 0.254829592f));
+    h = mul2(mul2(q, t), e);
+}
+
+// z Phi(z) = max(z, 0) - |z| h.  The factor |z| is capped where h is 0 already,
+// so that an infinite z gives infinity (or 0) and not infinity times 0.
+__device__ __forceinline__ float2 gelu2(float2 z) {
+    float2 h, e;
+    normal_tail(z, h, e);
+    return make_float2(fmaf(-fminf(fabsf(z.x), 32.0f), h.x, fmaxf(z.x, 0.0f)),
+                       fmaf(-fminf(fabsf(z.y), 32.0f), h.y, fmaxf(z.y, 0.0f)));
+}
+
+// Phi(z) + z phi(z); Phi(z) = 1/2 + (1/2 - h) with z's sign
+__device__ __forceinline__ float2 gelu_slope2(float2 z) {
+    float2 h, e;
+    normal_tail(z, h, e);
+    const float2 c = make_float2(0.5f + copysignf(0.5f - h.x, z.x), 0.5f + copysignf(0.5f - h.y, z.y));
+    return make_float2(fmaf(z.x * 0.39894228f, e.x, c.x), fmaf(z.y * 0.39894228f, e.y, c.y));
 }
 
 // act of N values.  The choice is made once for all of them, so the code that
@@ -54,25 +102,34 @@ __device__ __forceinline__ void act_values(int act, float (&v)[N]) {
         for (int i = 0; i < N; ++i) v[i] *= sigmoid_fast(v[i]);
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float e;
-            v[i] *= normal_cdf(v[i], e);
+        for (int i = 0; i < N; i += 2) {
+            const float2 y = gelu2(make_float2(v[i], v[i + 1]));
+            v[i] = y.x;
+            v[i + 1] = y.y;
         }
     }
 }
 
-__device__ __forceinline__ float act_slope(int act, float z) {
-    if (act == MOE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == MOE_ACT_SILU) {
-        const float s = sigmoid_fast(z);
-        return s * fmaf(z, 1.0f - s, 1.0f);
+// v *= act'(z) for N values
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, float (&v)[N], const float (&z)[N]) {
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = z[i] > 0.0f ? v[i] : 0.0f;
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float s = sigmoid_fast(z[i]);
+            v[i] *= s * fmaf(z[i], 1.0f - s, 1.0f);
+        }
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 d = gelu_slope2(make_float2(z[i], z[i + 1]));
+            v[i] *= d.x;
+            v[i + 1] *= d.y;
+        }
     }
-    if (act == MOE_ACT_GELU) {
-        float e;
-        const float c = normal_cdf(z, e);
-        return fmaf(z * 0.39894228f, e, c);
-    }
-    return 1.0f;
 }
 
 }  // namespace moe

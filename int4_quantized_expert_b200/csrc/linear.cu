@@ -37,7 +37,14 @@
 // LIN_SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
 // shares one tile's contraction.  Each leaves its partial sums in its shared
 // memory, and the CTAs add each other's through distributed shared memory in
-// rank order: no scratch, no atomics, the same bits every time.
+// rank order: no scratch, no atomics, the same bits every time.  Such calls are
+// short and bound by the weights' bytes, so what counts is how soon a call's
+// loads follow the last call's: tiles of up to 64 columns take half of an SM's
+// shared memory and 64 columns of tensor memory, so that the next call's CTAs
+// (programmatic dependent launch) are set up and waiting beside this one's.
+//
+// Without offsets, a CTA knows its weights before it has waited for the kernel
+// before it, and asks for a ring's worth of them to be brought into L2.
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 slot hand-over (LIN_DW: zeroes rows;
 // LIN_PAIR: tells the MMA issuer's CTA that its own half has landed), 3
@@ -56,14 +63,13 @@
 namespace moe {
 
 constexpr int LN_THREADS = 384;
-constexpr int LN_EPI_WARPS = 8;
-constexpr int LN_MAX_STAGES = 8;
+constexpr int LN_EPI_WARPS = 8, LN_EPI_THREADS = 32 * LN_EPI_WARPS;
+constexpr int LN_MAX_STAGES = 10;
 constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
-constexpr int LN_RING_BYTES = 196608;     // 4 slots of 48 KB, 6 of 32 KB or 8 of 24 KB
-constexpr int LN_TMEM_COLS = 512;
+constexpr int LN_RING_BYTES = 196608;     // the ring of a CTA that has an SM to itself
+constexpr int LN_HALF_RING_BYTES = 106496;   // of one that shares it with another
 constexpr int LN_STG_BYTES = 32 * 64;     // an epilogue warp's staging buffer: 32 columns x 32 features, bf16
-static_assert(LN_RING_BYTES >= 256 * 128 * 4, "the partial sums of a split tile reuse the ring");
 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
 static __device__ int32_t g_linear_status;
@@ -85,9 +91,12 @@ struct LinSmem {
     int32_t begin[LN_MAX_E];         // the expert's rows
     int32_t count[LN_MAX_E];
     int32_t warp_sum[LN_THREADS / 32];
-    alignas(128) unsigned char stage[LN_EPI_WARPS][LN_STG_BYTES];
 };
-static_assert(1024 + LN_RING_BYTES + sizeof(LinSmem) <= 232448, "shared memory of a block");
+// behind it, unless SPLIT: the epilogue warps' staging buffers
+constexpr int LN_STG_OFFSET = (int(sizeof(LinSmem)) + 127) & ~127;
+constexpr int LN_SMEM_BYTES = 1024 + LN_RING_BYTES + LN_STG_OFFSET + LN_EPI_WARPS * LN_STG_BYTES;
+static_assert(LN_SMEM_BYTES <= 232448, "shared memory of a block");
+static_assert(2 * (1024 + 1024 + LN_HALF_RING_BYTES + LN_STG_OFFSET) <= 233472, "two blocks on an SM");
 
 // Shared-memory matrix descriptor of an MN-major tile with the 128-byte
 // swizzle: rows of 64 values along M or N (128 bytes), one per c; 8 c are
@@ -142,8 +151,8 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
         t.clen = p.C;
     }
     const int nk = (t.clen + 63) >> 6;
-    t.k0 = SPLIT ? int(int64_t(nk) * rank / p.split) : 0;
-    t.k1 = SPLIT ? int(int64_t(nk) * (rank + 1) / p.split) : nk;
+    t.k0 = SPLIT ? nk * rank / p.split : 0;
+    t.k1 = SPLIT ? nk * (rank + 1) / p.split : nk;
     return t;
 }
 
@@ -151,7 +160,7 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
 // activation, residual, rounding, store.  idx: of the first one in the output.
 template <int MODE>
 __device__ __forceinline__ void finish8(const LinParams& p, int64_t idx, float (&v)[8], const uint4& bias,
-                                        const uint4& res) {
+                                        const uint4& res) {   // bias, res: read where p has them
     if (MODE == LIN_FWD) {
         if (p.bias) {
             float t[8];
@@ -289,12 +298,12 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(const float* p, uint32_t rank) 
 }
 
 template <int MODE, int SHARE>
-__global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ CUtensorMap tm_a,
+__global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear_kernel(const __grid_constant__ CUtensorMap tm_a,
                                                                const __grid_constant__ CUtensorMap tm_b, LinParams p) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* base = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    LinSmem* sm = reinterpret_cast<LinSmem*>(base + LN_RING_BYTES);
+    LinSmem* sm = reinterpret_cast<LinSmem*>(base + p.ring_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
     constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
@@ -305,27 +314,28 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     const bool leader = !PAIR || rank == 0;   // issues the MMAs
 
     griddep_launch_dependents();
-    if (threadIdx.x == 0) {
-        prefetch_tmap(&tm_a);
-        prefetch_tmap(&tm_b);
-        for (int i = 0; i < LN_MAX_STAGES; ++i) {
-            mbar_init(&sm->full[i], 1);
-            mbar_init(&sm->empty[i], 1);
-            mbar_init(&sm->ready[i], PAIR ? 2 : 1);
+    if (warp == 0) {
+        if (lane < LN_MAX_STAGES) {
+            mbar_init(&sm->full[lane], 1);
+            mbar_init(&sm->empty[lane], 1);
+            mbar_init(&sm->ready[lane], PAIR ? 2 : 1);
+        } else if (lane < LN_MAX_STAGES + 2) {
+            mbar_init(&sm->acc_full[lane - LN_MAX_STAGES], 1);
+            mbar_init(&sm->acc_empty[lane - LN_MAX_STAGES], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
+        } else if (lane == LN_MAX_STAGES + 2) {
+            mbar_init(&sm->drained, 1);
+            sm->status = DEV_OK;
+        } else if (lane == LN_MAX_STAGES + 3) {
+            prefetch_tmap(&tm_a);
+            prefetch_tmap(&tm_b);
         }
-        mbar_init(&sm->drained, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm->acc_full[i], 1);
-            mbar_init(&sm->acc_empty[i], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
-        }
-        sm->status = DEV_OK;
         fence_barrier_init();
     }
     if (warp == 3) {
-        tmem_alloc<PAIR>(&sm->tmem_base, LN_TMEM_COLS);
+        tmem_alloc<PAIR>(&sm->tmem_base, p.tmem_cols);
         tmem_relinquish<PAIR>();
     }
-    griddep_wait();
+    if (p.offsets) griddep_wait();
 
     // the row ranges, and for LIN_FWD / LIN_DX the chunks before each expert
     int chunks = 0;
@@ -369,22 +379,45 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
     const int n_tiles = n_units * p.n_fblocks;
     const int tile0 = SPLIT ? int(blockIdx.x) / p.split : PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
-    // a split tile is its cluster's only one
     const int tstep = SPLIT ? INT_MAX / 2 : PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
     // the MMA's N, and the rows of B (the columns of D) that this CTA loads
     auto mma_n = [](const Tile& t) { return PAIR ? (t.ncols + 31) & ~31 : (t.ncols + 15) & ~15; };
     auto b_first = [&](const Tile& t) { return PAIR ? int(rank) * (mma_n(t) / 2) : 0; };
-    auto b_boxes = [&](const Tile& t) { return ((PAIR ? mma_n(t) / 2 : t.ncols) + 63) >> 6; };
+    auto b_boxes = [&](const Tile& t) { return ((PAIR ? mma_n(t) / 2 : t.ncols) + p.box - 1) / p.box; };
+
+    int tile = tile0;
+    Tile t = {};
+    if (tile < n_tiles) t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+    auto advance = [&] {
+        tile += tstep;
+        if (tile < n_tiles) t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+    };
+
+    uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;   // SPLIT: this thread's pieces of them
+    if (!p.offsets) {
+        if (MODE != LIN_DW && warp == 0 && tile < n_tiles && elect_one()) {
+            for (int kk = t.k0; kk < t.k1 && kk < t.k0 + p.stages; ++kk) {
+                if (MODE == LIN_FWD) {
+                    tma_prefetch_3d(&tm_a, kk * 64, t.f0, t.e);
+                } else {
+                    tma_prefetch_3d(&tm_a, t.f0, kk * 64, t.e);
+                    tma_prefetch_3d(&tm_a, t.f0 + 64, kk * 64, t.e);
+                }
+            }
+        }
+        __syncwarp();
+        griddep_wait();
+    }
 
     if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
         if (elect_one()) {
             uint32_t slot = 0, par = 1, filled = 0;
             bool ok = true;
-            for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-                const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+            for (; tile < n_tiles && ok; advance()) {
                 const int boxes = b_boxes(t), row = t.col0 + b_first(t);
-                const uint32_t bytes = LN_A_BYTES + boxes * 8192;
+                const int box_bytes = p.box * 128;
+                const uint32_t bytes = LN_A_BYTES + boxes * box_bytes;
                 for (int kk = t.k0; kk < t.k1; ++kk) {
                     if (!mbar_wait(&sm->empty[slot], par, &sm->status)) { ok = false; break; }
                     unsigned char* sa = base + slot * stage_bytes;
@@ -403,7 +436,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     }
                     for (int i = 0; i < boxes; ++i) {
                         if (B_MN) tma_load_2d(sb + i * 8192, &tm_b, bar, row + i * 64, c);
-                        else tma_load_2d(sb + i * 8192, &tm_b, bar, c, row + i * 64);
+                        else tma_load_2d(sb + i * box_bytes, &tm_b, bar, c, row + i * p.box);
                     }
                     ++filled;
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
@@ -420,8 +453,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         if (leader && elect_one()) {
             uint32_t slot = 0, par = 0, n = 0;
             bool ok = true;
-            for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-                const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+            for (; tile < n_tiles && ok; advance()) {
                 if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
                 const uint32_t idesc = tc_idesc_fmt(PAIR ? 256 : 128, mma_n(t), 1u) |
                                        (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
@@ -465,8 +497,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         // ---------------- hand the slots over to the MMA issuer ----------------
         uint32_t slot = 0, par = 0;
         bool ok = true;
-        for (int tile = tile0; tile < n_tiles && ok; tile += tstep) {
-            const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+        for (; tile < n_tiles && ok; advance()) {
             const int boxes = b_boxes(t);
             for (int kk = t.k0; kk < t.k1; ++kk) {
                 if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
@@ -495,17 +526,23 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     } else if (warp >= 4) {
         // ------------------------------ epilogue ------------------------------
         const int ew = warp & 3;                 // TMEM lanes 32 ew .. 32 ew + 31
+        const uint32_t stage = smem_u32(sm) + LN_STG_OFFSET + (warp - 4) * LN_STG_BYTES;
         uint32_t n = 0;
-        for (int tile = tile0; tile < n_tiles; tile += tstep) {
-            const Tile t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+        for (; tile < n_tiles; advance()) {
             const bool any = t.k0 < t.k1;
             const uint32_t acc = n & 1;
+            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
+            if (SPLIT && MODE == LIN_FWD) {   // under the sums: what the end of the tile reads besides them
+                const int f = t.f0 + 8 * (threadIdx.x & 15), col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16;
+                if (p.bias && f < p.F) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
+                if (p.residual && f < p.F && col < t.ncols)
+                    res0 = *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
+            }
             if (any) {
                 if (!mbar_wait(&sm->acc_full[acc], (n >> 1) & 1, &sm->status)) break;
                 tc_fence_after();
             }
             const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
-            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             if (SPLIT) {   // partial sums [col][128], added up below
                 for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
                     uint32_t v[32];
@@ -517,8 +554,10 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     }
                     float* red = reinterpret_cast<float*>(base) + cc * 32 * 128 + ew * 32 + lane;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) red[j * 128] = __uint_as_float(v[j]);
+                    for (int j = 0; j < 32; ++j)
+                        if (cc * 32 + j < t.ncols) red[j * 128] = __uint_as_float(v[j]);
                 }
+                break;     // a split tile is its cluster's only one
             } else {
                 // every other 32 columns for each of the two warps of these lanes
                 auto release = [&] {
@@ -546,40 +585,40 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     if (cc + 2 >= nb) release();
                     else if (any) tmem_ld_block(taddr + cc * 32 + 64, v);
                     finish_block<MODE>(p, a, row0 + cc * 32, t.ncols - cc * 32, t.f0 + ew * 32,
-                                       smem_u32(sm->stage[warp - 4]), lane);
+                                       stage, lane);
                 }
             }
             if (any) ++n;
         }
     }
     if (SPLIT) {
+        // every CTA's partial sums are in its shared memory
         __syncwarp();
-        cluster_sync();                          // every CTA's partial sums are in its shared memory
-        if (tile0 < n_tiles) {
-            const Tile t = get_tile<MODE, SHARE>(tile0, sm, p, n_units, rank);
+        if (p.split > 1) cluster_sync();
+        else __syncthreads();
+        if (warp >= 4 && tile < n_tiles) {
+            // 16 threads to a column, each with eight features
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
-            const float* red = reinterpret_cast<const float*>(base);
-            for (int i = int(rank) * LN_THREADS + int(threadIdx.x); i < t.ncols * 16; i += p.split * LN_THREADS) {
-                const int col = i >> 4, f = t.f0 + 8 * (i & 15);
-                if (f >= p.F) continue;
+            const int f8 = 8 * (threadIdx.x & 15), f = t.f0 + f8, step = p.split * (LN_EPI_THREADS / 16);
+            const float* red = reinterpret_cast<const float*>(base) + f8;
+            for (int col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16; col < t.ncols && f < p.F; col += step) {
                 const int64_t idx = (row0 + col) * p.F + f;
-                uint4 bias = make_uint4(0, 0, 0, 0), res = bias;
-                if (MODE == LIN_FWD) {
-                    if (p.bias) bias = *reinterpret_cast<const uint4*>(p.bias + f);
-                    if (p.residual) res = *reinterpret_cast<const uint4*>(p.residual + idx);
-                }
+                const uint4 res = res0;
+                if (MODE == LIN_FWD && p.residual && col + step < t.ncols)
+                    res0 = *reinterpret_cast<const uint4*>(p.residual + idx + int64_t(step) * p.F);
                 float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
                 for (int s = 0; s < p.split; ++s) {
-                    const float4 a = ld_dsmem_f32x4(red + col * 128 + 8 * (i & 15), s);
-                    const float4 b = ld_dsmem_f32x4(red + col * 128 + 8 * (i & 15) + 4, s);
+                    const float4 a = ld_dsmem_f32x4(red + col * 128, s);
+                    const float4 b = ld_dsmem_f32x4(red + col * 128 + 4, s);
                     v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
                     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
                 }
-                finish8<MODE>(p, idx, v, bias, res);
+                finish8<MODE>(p, idx, v, bias0, res);
             }
         }
         __syncwarp();
-        cluster_sync();                          // no CTA leaves while another reads its shared memory
+        if (p.split > 1) cluster_sync();         // no CTA leaves while another reads its shared memory
     }
     if (PAIR) {
         __syncwarp();
@@ -591,7 +630,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
     __syncthreads();
     if (warp == 3) {
         tc_fence_after();
-        tmem_dealloc<PAIR>(tmem, LN_TMEM_COLS);
+        tmem_dealloc<PAIR>(tmem, p.tmem_cols);
     }
     if (threadIdx.x == 0 && sm->status != DEV_OK) atomicOr(&g_linear_status, sm->status);
 }
@@ -624,23 +663,13 @@ __global__ void __launch_bounds__(AG_THREADS) act_grad_kernel(const bf16* __rest
 #pragma unroll 4
         for (int r = r0 + rl; r < r1; r += 32) {
             const int64_t idx = int64_t(r) * N + col;
-            const uint4 d = *reinterpret_cast<const uint4*>(dy + idx);
-            const uint32_t dw[4] = {d.x, d.y, d.z, d.w};
             float v[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(dw[i]); v[2 * i + 1] = bf16_hi(dw[i]); }
+            unpack8(*reinterpret_cast<const uint4*>(dy + idx), v);
             if (DZ) {
-                const uint4 q = *reinterpret_cast<const uint4*>(z + idx);
-                const uint32_t zw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    v[2 * i] *= act_slope(act, bf16_lo(zw[i]));
-                    v[2 * i + 1] *= act_slope(act, bf16_hi(zw[i]));
-                }
-                if (dz)
-                    *reinterpret_cast<uint4*>(dz + idx) =
-                        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                                   pack_bf16x2(v[6], v[7]));
+                float zv[8];
+                unpack8(*reinterpret_cast<const uint4*>(z + idx), zv);
+                act_slopes(act, v, zv);
+                if (dz) *reinterpret_cast<uint4*>(dz + idx) = pack8(v);
             }
             if (DB)
 #pragma unroll
@@ -728,15 +757,33 @@ moe_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned bloc
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
 }
 
+// As much shared memory as two blocks need, once per device (see allow_max_smem).
+template <typename... KArgs>
+moe_status prefer_smem(void (*kernel)(KArgs...)) {
+    static std::mutex mu;
+    static std::set<std::pair<const void*, int>> done;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
+    if (done.count(key)) return MOE_OK;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    done.insert(key);
+    return MOE_OK;
+}
+
 template <int MODE>
-moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, bool pair, int64_t tiles,
+moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int share, int64_t tiles,
                        int sms, cudaStream_t stream) {
-    const size_t smem = 1024 + LN_RING_BYTES + sizeof(LinSmem);
-    auto kernel = pair          ? linear_kernel<MODE, LIN_PAIR>
-                  : p.split > 1 ? linear_kernel<MODE, LIN_SPLIT>
-                                : linear_kernel<MODE, LIN_ONE>;
-    if (allow_max_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
-    const int64_t cluster = pair ? 2 : p.split, grid = p.split > 1 ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
+    auto kernel = share == LIN_PAIR    ? linear_kernel<MODE, LIN_PAIR>
+                  : share == LIN_SPLIT ? linear_kernel<MODE, LIN_SPLIT>
+                                       : linear_kernel<MODE, LIN_ONE>;
+    if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
+    const size_t smem = 1024 + p.ring_bytes + LN_STG_OFFSET + (share == LIN_SPLIT ? 0 : LN_EPI_WARPS * LN_STG_BYTES);
+    const int64_t cluster = share == LIN_PAIR ? 2 : share == LIN_SPLIT ? p.split : 1;
+    const int64_t grid = share == LIN_SPLIT ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
     return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, smem, unsigned(cluster), stream, ta, tb, p);
 }
 
@@ -750,35 +797,47 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
     p.F = mode == LIN_FWD ? N : K;
     p.C = mode == LIN_FWD ? K : N;
     p.NC = N;
-    // columns of a tile: as many as an expert has rows on average (LIN_FWD,
-    // LIN_DX) or as there are (LIN_DW); few columns leave room for more slots
-    const int64_t cols = mode == LIN_DW ? N : ceil_div(p.rows, p.E);
-    p.bn = cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
+    // columns of a tile: as many as there are (LIN_DW: n), or as an expert has
+    // rows on average -- and not below 64 then, since many rows of one expert in
+    // narrow tiles would stream its weights through every SM again and again
+    int64_t cols = mode == LIN_DW ? N : p.rows;
+    if (mode != LIN_DW && p.offsets && cols > 64) cols = ceil_div(p.rows, p.E) > 64 ? ceil_div(p.rows, p.E) : 64;
+    p.bn = cols <= 16 && mode != LIN_DW ? 16 : cols <= 32 && mode != LIN_DW ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
     const int64_t units = mode == LIN_DW ? p.E * ceil_div(N, p.bn)
                           : p.offsets    ? p.rows / p.bn + (p.E < p.rows ? p.E : p.rows)   // at most
                                          : ceil_div(p.rows, p.bn);
-    // wide tiles go to pairs of CTAs, unless there are so few that more than
-    // half of the pairs had none
-    const bool pair = p.bn == 256 && 2 * units * ceil_div(p.F, 256) > sms / 2;
-    p.stages = LN_RING_BYTES / (LN_A_BYTES + (pair ? p.bn / 2 : p.bn) * 128);
-    p.n_fblocks = int(ceil_div(p.F, pair ? 256 : 128));
-    const int64_t tiles = units * p.n_fblocks;
+    const int64_t tiles = units * ceil_div(p.F, 128);
     const int64_t steps = ceil_div(mode == LIN_DW ? ceil_div(p.rows, p.E) : p.C, 64);
+    // wide tiles go to pairs of CTAs, unless there are so few that more than
+    // half of the pairs had none; few tiles are split along the contraction
+    int share = LIN_ONE;
     p.split = 1;
-    if (!pair && 2 * tiles <= sms) {
+    if (p.bn == 256 && 2 * units * ceil_div(p.F, 256) > sms / 2) {
+        share = LIN_PAIR;
+    } else if (p.bn <= 64 ? tiles <= sms : 2 * tiles <= sms) {
+        share = LIN_SPLIT;
         int64_t s = sms / tiles;
         if (s > 8) s = 8;
         if (s > steps / 4) s = steps / 4;
         if (s > 1) p.split = int(s);
     }
+    p.n_fblocks = int(ceil_div(p.F, share == LIN_PAIR ? 256 : 128));
+    p.box = mode == LIN_DW ? 64 : share == LIN_PAIR ? 32 : p.bn < 64 ? p.bn : 64;
+    const int stage = LN_A_BYTES + (share == LIN_PAIR ? p.bn / 2 : p.bn) * 128;
+    const bool half = share == LIN_SPLIT && p.bn <= 64;
+    p.stages = (half ? LN_HALF_RING_BYTES : LN_RING_BYTES) / stage;
+    if (p.stages > LN_MAX_STAGES) p.stages = LN_MAX_STAGES;
+    p.ring_bytes = p.stages * stage;
+    if (share == LIN_SPLIT && p.ring_bytes < p.bn * 512) p.ring_bytes = p.bn * 512;   // its partial sums reuse the ring
+    p.tmem_cols = share == LIN_SPLIT ? (p.bn < 32 ? 32 : p.bn) : 512;
     CUtensorMap ta, tb;
     const bool ok = mode == LIN_DW
         ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
-        : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, 64);
+        : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, p.box);
     if (!ok) return MOE_ERR_CUDA;
-    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, pair, tiles, sms, stream);
-    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, pair, tiles, sms, stream);
-    return launch_mode<LIN_DW>(ta, tb, p, pair, tiles, sms, stream);
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
+    return launch_mode<LIN_DW>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
 }
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
