@@ -15,8 +15,8 @@
 //
 // Tiles: 128 features x up to bn columns, steps of 64 along c, through a ring
 // of TMA-filled slots (A 16 KB, B bn x 128 B, 128-byte swizzle).  D is fp32 in
-// tensor memory, two accumulators, so a tile's epilogue overlaps the next
-// tile's MMAs.  TMA's zero fill pads c, features and rows at the tensors'
+// tensor memory, whose 512 columns are handed out in turn, so a tile's epilogue
+// overlaps the next tile's MMAs.  TMA's zero fill pads c, features and rows at the tensors'
 // edges; what it cannot pad is the end of an expert's rows inside the tensor
 // when c runs over rows (LIN_DW): warp 2 zeroes those rows of both operands
 // in the slot before the MMAs read it, so rows of the next expert -- which may
@@ -31,7 +31,10 @@
 //
 // An expert's rows are cut into equal chunks of at most bn rows (rounded up to
 // 16), not into full chunks and a tail: a tail of a few rows would stream a
-// whole weight tile for them.  Each CTA derives the list from the offsets by a
+// whole weight tile for them.  A pair's tile may have up to 320 rows, as two
+// accumulators (192 columns and the rest) under one pass over the weights: 300
+// rows in two tiles of 160 would load the weights twice, and the 64 bytes a
+// cycle that an SM can load are what bounds narrow tiles.  Each CTA derives the list from the offsets by a
 // scan over the (at most 256) experts.
 //
 // LIN_SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
@@ -48,13 +51,15 @@
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 slot hand-over (LIN_DW: zeroes rows;
 // LIN_PAIR: tells the MMA issuer's CTA that its own half has landed), 3
-// tensor-memory allocation, 4-11 epilogue.  The single threads of warps 0 and
-// 1 are picked by elect.sync: under `lane == 0` the TMA and MMA instructions'
-// uniform operands cost about 200 cycles each (708 cycles a step of three
-// loads against the MMAs' 512; 525 a step of both with elect.sync).
+// tensor-memory allocation, 4-11 epilogue.  The single threads of warps 0 and 1
+// are picked by elect.sync and run their loops alone: under `lane == 0` a step's
+// three loads took 708 cycles to issue, against the MMAs' 512, and with loops
+// run by the whole warp on shuffled (uniform) values a step of loads and MMAs
+// took 710; this way it takes 530.
 #include <cuda.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "activation.cuh"
 #include "linear.cuh"
@@ -65,6 +70,8 @@ namespace moe {
 constexpr int LN_THREADS = 384;
 constexpr int LN_EPI_WARPS = 8, LN_EPI_THREADS = 32 * LN_EPI_WARPS;
 constexpr int LN_MAX_STAGES = 10;
+constexpr int LN_ACCS = 4;                // accumulators in use at a time
+constexpr int LN_SUB = 192;               // columns of the first accumulator of a tile of more than 256
 constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
 constexpr int LN_RING_BYTES = 196608;     // the ring of a CTA that has an SM to itself
@@ -83,8 +90,8 @@ struct LinSmem {
     uint64_t empty[LN_MAX_STAGES];   // the slot's MMAs completed
     uint64_t ready[LN_MAX_STAGES];   // LIN_DW, LIN_PAIR: warp 2 (of both CTAs) handed the slot over
     uint64_t drained;                // all MMAs of this CTA (pair) completed
-    uint64_t acc_full[2];            // accumulator holds a finished tile
-    uint64_t acc_empty[2];           // epilogue (of both CTAs) finished reading the accumulator
+    uint64_t acc_full[LN_ACCS];      // accumulator holds a finished tile
+    uint64_t acc_empty[LN_ACCS];     // epilogue (of both CTAs) finished reading the accumulator
     uint32_t tmem_base;
     int32_t status;                  // of this CTA; joined into g_linear_status at the end
     int32_t first[LN_MAX_E + 1];     // chunks before each expert (LIN_FWD, LIN_DX)
@@ -110,6 +117,25 @@ struct Tile {
     int e, f0;            // the CTA's first feature
     int col0, ncols;      // output rows (LIN_FWD, LIN_DX: rows; LIN_DW: n) of the tile
     int c0, k0, k1, clen; // contraction: first row (LIN_DW), steps [k0, k1), length
+};
+
+// Chunks of an expert's rows.  Tiles of up to 320 rows save a pass over the
+// weights where few chunks of up to 256 would be narrow.
+__device__ __forceinline__ int row_chunks(int rows, int bn) {
+    if (bn <= 256) return (rows + bn - 1) / bn;
+    const int c = (rows + 255) >> 8, wide = (rows + 319) / 320;
+    return c <= 4 ? wide : c;
+}
+
+// The columns of tensor memory of each accumulator in turn: wherever the last
+// one ended, or from the start again.
+struct AccColumns {
+    int head = 0;
+    __device__ __forceinline__ int next(int width) {
+        const int first = head + width > 512 ? 0 : head;
+        head = first + width;
+        return first;
+    }
 };
 
 template <int MODE, int SHARE>
@@ -319,13 +345,13 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             mbar_init(&sm->full[lane], 1);
             mbar_init(&sm->empty[lane], 1);
             mbar_init(&sm->ready[lane], PAIR ? 2 : 1);
-        } else if (lane < LN_MAX_STAGES + 2) {
+        } else if (lane < LN_MAX_STAGES + LN_ACCS) {
             mbar_init(&sm->acc_full[lane - LN_MAX_STAGES], 1);
             mbar_init(&sm->acc_empty[lane - LN_MAX_STAGES], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
-        } else if (lane == LN_MAX_STAGES + 2) {
+        } else if (lane == LN_MAX_STAGES + LN_ACCS) {
             mbar_init(&sm->drained, 1);
             sm->status = DEV_OK;
-        } else if (lane == LN_MAX_STAGES + 3) {
+        } else if (lane == LN_MAX_STAGES + LN_ACCS + 1) {
             prefetch_tmap(&tm_a);
             prefetch_tmap(&tm_b);
         }
@@ -353,7 +379,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         }
         sm->begin[threadIdx.x] = b;
         sm->count[threadIdx.x] = c;
-        chunks = (c + p.bn - 1) / p.bn;
+        chunks = p.offsets ? row_chunks(c, p.bn) : p.chunks;
     }
     if (MODE != LIN_DW) {
         int incl = chunks;
@@ -380,10 +406,14 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     const int n_tiles = n_units * p.n_fblocks;
     const int tile0 = SPLIT ? int(blockIdx.x) / p.split : PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
     const int tstep = SPLIT ? INT_MAX / 2 : PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
-    // the MMA's N, and the rows of B (the columns of D) that this CTA loads
-    auto mma_n = [](const Tile& t) { return PAIR ? (t.ncols + 31) & ~31 : (t.ncols + 15) & ~15; };
-    auto b_first = [&](const Tile& t) { return PAIR ? int(rank) * (mma_n(t) / 2) : 0; };
-    auto b_boxes = [&](const Tile& t) { return ((PAIR ? mma_n(t) / 2 : t.ncols) + p.box - 1) / p.box; };
+    // the accumulators of a tile: MMA's N, and the rows of B (the columns of D)
+    // that this CTA loads
+    constexpr bool WIDE = PAIR && MODE != LIN_DW;
+    auto subs = [](const Tile& t) { return WIDE && t.ncols > 256 ? 2 : 1; };
+    auto sub_cols = [&](const Tile& t, int i) { return subs(t) == 1 ? t.ncols : i == 0 ? LN_SUB : t.ncols - LN_SUB; };
+    auto mma_n = [](int ncols) { return PAIR ? (ncols + 31) & ~31 : (ncols + 15) & ~15; };
+    auto b_rows = [&](int ncols) { return PAIR ? mma_n(ncols) / 2 : ncols; };
+    auto b_boxes = [&](int ncols) { return (b_rows(ncols) + p.box - 1) / p.box; };
 
     int tile = tile0;
     Tile t = {};
@@ -415,7 +445,10 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             uint32_t slot = 0, par = 1, filled = 0;
             bool ok = true;
             for (; tile < n_tiles && ok; advance()) {
-                const int boxes = b_boxes(t), row = t.col0 + b_first(t);
+                const int n0 = sub_cols(t, 0), n1 = subs(t) > 1 ? t.ncols - n0 : 0;
+                const int boxes0 = b_boxes(n0), boxes = boxes0 + (WIDE ? b_boxes(n1) : 0);
+                const int row = t.col0 + (PAIR ? int(rank) * b_rows(n0) : 0);
+                const int row1 = t.col0 + n0 + int(rank) * b_rows(n1) - boxes0 * p.box;   // so box i is at row1 + i * p.box
                 const int box_bytes = p.box * 128;
                 const uint32_t bytes = LN_A_BYTES + boxes * box_bytes;
                 for (int kk = t.k0; kk < t.k1; ++kk) {
@@ -423,8 +456,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     unsigned char* sa = base + slot * stage_bytes;
                     unsigned char* sb = sa + LN_A_BYTES;
                     uint64_t* bar = &sm->full[slot];
-                    mbar_arrive_expect_tx(bar, bytes);
                     const int c = t.c0 + kk * 64;
+                    mbar_arrive_expect_tx(bar, bytes);
                     if (MODE == LIN_FWD) {
                         tma_load_3d(sa, &tm_a, bar, c, t.f0, t.e);
                     } else if (MODE == LIN_DX) {
@@ -436,7 +469,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     }
                     for (int i = 0; i < boxes; ++i) {
                         if (B_MN) tma_load_2d(sb + i * 8192, &tm_b, bar, row + i * 64, c);
-                        else tma_load_2d(sb + i * box_bytes, &tm_b, bar, c, row + i * p.box);
+                        else tma_load_2d(sb + i * box_bytes, &tm_b, bar, c, (!WIDE || i < boxes0 ? row : row1) + i * p.box);
                     }
                     ++filled;
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
@@ -451,18 +484,32 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         if (leader && elect_one()) {
-            uint32_t slot = 0, par = 0, n = 0;
+            uint32_t slot = 0, par = 0, n = 0, done = 0;   // accumulators begun; known to be free again
+            uint32_t held = 0;                             // columns of the last four: first / 32 and width / 32 - 1
+            AccColumns cols;
             bool ok = true;
-            for (; tile < n_tiles && ok; advance()) {
-                if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
-                const uint32_t idesc = tc_idesc_fmt(PAIR ? 256 : 128, mma_n(t), 1u) |
-                                       (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-                const uint32_t acc = n & 1;
-                if (!mbar_wait(&sm->acc_empty[acc], ((n >> 1) & 1) ^ 1, &sm->status)) { ok = false; break; }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem + acc * 256;
+            const uint32_t idesc_m = tc_idesc_fmt(PAIR ? 256 : 128, 0, 1u) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+            // the columns of the next accumulator, once they are free: the one
+            // that had its barrier before and all that had these columns are read
+            auto take = [&](int nn) {
+                const int width = (nn + 31) & ~31, first = cols.next(width);
+                uint32_t need = n >= LN_ACCS ? n - LN_ACCS + 1 : 0;
+                for (uint32_t j = max(done, need); j < n; ++j) {
+                    const uint32_t h = held >> (8 * (j % LN_ACCS));
+                    const int hf = 32 * (h & 15), hw = 32 * ((h >> 4 & 15) + 1);
+                    if (first < hf + hw && hf < first + width) need = j + 1;
+                }
+                for (; done < need && ok; ++done)
+                    ok = mbar_wait(&sm->acc_empty[done % LN_ACCS], (done / LN_ACCS) & 1, &sm->status);
+                const int at = 8 * (n % LN_ACCS);
+                held = (held & ~(255u << at)) | uint32_t((first >> 5) | ((width >> 5) - 1) << 4) << at;
+                ++n;
+                return tmem + first;
+            };
+            // the steps of a tile, with one or two accumulators
+            auto steps = [&](auto two, uint32_t d0, uint32_t idesc0, uint32_t d1, uint32_t idesc1) {
                 for (int kk = t.k0; kk < t.k1; ++kk) {
-                    if (!mbar_wait(HAND_OVER ? &sm->ready[slot] : &sm->full[slot], par, &sm->status)) { ok = false; break; }
+                    if (!mbar_wait(HAND_OVER ? &sm->ready[slot] : &sm->full[slot], par, &sm->status)) return false;
                     const int left = t.clen - kk * 64;
                     // the peer's zeroes: this wait acquires at CTA scope only
                     if (PAIR && MODE == LIN_DW && left < 64) asm volatile("fence.acq_rel.cluster;" ::: "memory");
@@ -475,18 +522,29 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                         if (k16 * 16 < left) {
                             const uint64_t a = ad + (A_MN ? 128 : 2) * k16, b = bd + (B_MN ? 128 : 2) * k16;
                             const uint32_t accumulate = kk != t.k0 || k16 != 0;
-                            if (PAIR) umma_pair(d_tmem, a, b, idesc, accumulate);
-                            else umma<false>(d_tmem, a, b, idesc, accumulate);
+                            if (PAIR) umma_pair(d0, a, b, idesc0, accumulate);
+                            else umma<false>(d0, a, b, idesc0, accumulate);
+                            if (decltype(two)::value) umma_pair(d1, a, b + (LN_SUB / 2 * 128 >> 4), idesc1, accumulate);
                         }
                     if (PAIR) umma_commit_pair(&sm->empty[slot]);
                     else umma_commit(&sm->empty[slot]);
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
                 }
-                if (ok) {
-                    if (PAIR) umma_commit_pair(&sm->acc_full[acc]);
-                    else umma_commit(&sm->acc_full[acc]);
-                }
-                ++n;
+                return true;
+            };
+            for (; tile < n_tiles && ok; advance()) {
+                if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
+                const int n0 = mma_n(sub_cols(t, 0)), n1 = subs(t) > 1 ? mma_n(sub_cols(t, 1)) : 0;
+                const uint32_t idesc0 = idesc_m | uint32_t(n0 >> 3) << 17, idesc1 = idesc_m | uint32_t(n1 >> 3) << 17;
+                const uint32_t d0 = take(n0), d1 = WIDE && n1 ? take(n1) : 0;
+                if (!ok) break;
+                tc_fence_after();
+                if (WIDE && n1) ok = steps(std::true_type{}, d0, idesc0, d1, idesc1);
+                else ok = steps(std::false_type{}, d0, idesc0, 0, 0);
+                if (!ok) break;
+                if (WIDE && n1) umma_commit_pair(&sm->acc_full[(n - 2) % LN_ACCS]);
+                if (PAIR) umma_commit_pair(&sm->acc_full[(n - 1) % LN_ACCS]);
+                else umma_commit(&sm->acc_full[(n - 1) % LN_ACCS]);
             }
             // wind down: wait (bounded) for the last MMAs
             if (PAIR) umma_commit_pair(&sm->drained);
@@ -498,7 +556,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         uint32_t slot = 0, par = 0;
         bool ok = true;
         for (; tile < n_tiles && ok; advance()) {
-            const int boxes = b_boxes(t);
+            const int boxes = b_boxes(t.ncols);   // LIN_DW
             for (int kk = t.k0; kk < t.k1; ++kk) {
                 if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
                 const int left = t.clen - kk * 64;
@@ -528,9 +586,9 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         const int ew = warp & 3;                 // TMEM lanes 32 ew .. 32 ew + 31
         const uint32_t stage = smem_u32(sm) + LN_STG_OFFSET + (warp - 4) * LN_STG_BYTES;
         uint32_t n = 0;
-        for (; tile < n_tiles; advance()) {
+        AccColumns cols;
+        for (bool ok = true; tile < n_tiles && ok; advance()) {
             const bool any = t.k0 < t.k1;
-            const uint32_t acc = n & 1;
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             if (SPLIT && MODE == LIN_FWD) {   // under the sums: what the end of the tile reads besides them
                 const int f = t.f0 + 8 * (threadIdx.x & 15), col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16;
@@ -538,16 +596,15 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 if (p.residual && f < p.F && col < t.ncols)
                     res0 = *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
             }
-            if (any) {
-                if (!mbar_wait(&sm->acc_full[acc], (n >> 1) & 1, &sm->status)) break;
-                tc_fence_after();
-            }
-            const uint32_t taddr = tmem + (uint32_t(32 * ew) << 16) + acc * 256;
             if (SPLIT) {   // partial sums [col][128], added up below
+                if (any) {
+                    if (!mbar_wait(&sm->acc_full[0], 0, &sm->status)) break;
+                    tc_fence_after();
+                }
                 for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
                     uint32_t v[32];
                     if (any) {
-                        tmem_ld32(taddr + cc * 32, v);
+                        tmem_ld32(tmem + (uint32_t(32 * ew) << 16) + cc * 32, v);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0u;
@@ -558,17 +615,26 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                         if (cc * 32 + j < t.ncols) red[j * 128] = __uint_as_float(v[j]);
                 }
                 break;     // a split tile is its cluster's only one
-            } else {
+            }
+            for (int sub = 0; sub < subs(t); ++sub) {
+                const int ncols = sub_cols(t, sub);
+                const int64_t row = row0 + (sub ? LN_SUB : 0);
+                uint32_t taddr = tmem + (uint32_t(32 * ew) << 16);
+                if (any) {
+                    taddr += cols.next((mma_n(ncols) + 31) & ~31);
+                    if (!mbar_wait(&sm->acc_full[n % LN_ACCS], (n / LN_ACCS) & 1, &sm->status)) { ok = false; break; }
+                    tc_fence_after();
+                }
                 // every other 32 columns for each of the two warps of these lanes
                 auto release = [&] {
                     tc_fence_before();
                     __syncwarp();
                     if (any && lane == 0) {
-                        if (PAIR) mbar_arrive_at(&sm->acc_empty[acc], 0);
-                        else mbar_arrive(&sm->acc_empty[acc]);
+                        if (PAIR) mbar_arrive_at(&sm->acc_empty[n % LN_ACCS], 0);
+                        else mbar_arrive(&sm->acc_empty[n % LN_ACCS]);
                     }
                 };
-                const int nb = (t.ncols + 31) >> 5;
+                const int nb = (ncols + 31) >> 5;
                 int cc = (warp - 4) >> 2;
                 uint32_t v[2][16];
                 if (cc >= nb) release();
@@ -584,11 +650,10 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     // stores; after the last one the accumulator is free
                     if (cc + 2 >= nb) release();
                     else if (any) tmem_ld_block(taddr + cc * 32 + 64, v);
-                    finish_block<MODE>(p, a, row0 + cc * 32, t.ncols - cc * 32, t.f0 + ew * 32,
-                                       stage, lane);
+                    finish_block<MODE>(p, a, row + cc * 32, ncols - cc * 32, t.f0 + ew * 32, stage, lane);
                 }
+                if (any) ++n;
             }
-            if (any) ++n;
         }
     }
     if (SPLIT) {
@@ -774,6 +839,25 @@ moe_status prefer_smem(void (*kernel)(KArgs...)) {
     return MOE_OK;
 }
 
+// Chunks of all rows for pairs: the fewest that take the least time, counted as
+// rounds of tiles over the pairs times the cycles of a step, which are those of
+// the MMAs (2 a column) or of the loads (128 rows of A and half of the columns,
+// 64 bytes a cycle), whichever are more.
+// A tile of more than 256 leaves the tensor cores idle for about 5000 cycles at
+// its end, until its first accumulator has been read.
+int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
+    const int least = int(ceil_div(rows, 320)), most = int(ceil_div(rows, 256)) + 8;
+    int best = least;
+    int64_t best_time = INT64_MAX;
+    for (int c = least; c <= most; ++c) {
+        const int n = (int(ceil_div(rows, c)) + 31) & ~31;
+        const int64_t tile = int64_t(steps) * (2 * n > n + 256 ? 2 * n : n + 256) + (n > 256 ? 5000 : 0);
+        const int64_t time = ceil_div(int64_t(c) * n_fblocks, pairs) * tile;
+        if (time < best_time) best = c, best_time = time;
+    }
+    return best;
+}
+
 template <int MODE>
 moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int share, int64_t tiles,
                        int sms, cudaStream_t stream) {
@@ -802,6 +886,7 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
     // narrow tiles would stream its weights through every SM again and again
     int64_t cols = mode == LIN_DW ? N : p.rows;
     if (mode != LIN_DW && p.offsets && cols > 64) cols = ceil_div(p.rows, p.E) > 64 ? ceil_div(p.rows, p.E) : 64;
+    // (up to 320 for pairs: see row_chunks)
     p.bn = cols <= 16 && mode != LIN_DW ? 16 : cols <= 32 && mode != LIN_DW ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
     const int64_t units = mode == LIN_DW ? p.E * ceil_div(N, p.bn)
                           : p.offsets    ? p.rows / p.bn + (p.E < p.rows ? p.E : p.rows)   // at most
@@ -822,6 +907,17 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
         if (s > 1) p.split = int(s);
     }
     p.n_fblocks = int(ceil_div(p.F, share == LIN_PAIR ? 256 : 128));
+    p.chunks = int(ceil_div(p.rows, p.bn));
+    int64_t n_units = units;
+    if (share == LIN_PAIR && mode != LIN_DW) {
+        if (p.offsets) {
+            p.bn = 320;
+        } else {
+            p.chunks = pair_chunks(p.rows, p.n_fblocks, int(steps), sms / 2);
+            n_units = p.chunks;
+            if (ceil_div(p.rows, p.chunks) > 256) p.bn = 320;
+        }
+    }
     p.box = mode == LIN_DW ? 64 : share == LIN_PAIR ? 32 : p.bn < 64 ? p.bn : 64;
     const int stage = LN_A_BYTES + (share == LIN_PAIR ? p.bn / 2 : p.bn) * 128;
     const bool half = share == LIN_SPLIT && p.bn <= 64;
@@ -835,9 +931,9 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
         ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
         : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, p.box);
     if (!ok) return MOE_ERR_CUDA;
-    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
-    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
-    return launch_mode<LIN_DW>(ta, tb, p, share, units * p.n_fblocks, sms, stream);
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
+    return launch_mode<LIN_DW>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
 }
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,

@@ -20,7 +20,8 @@ struct LinParams {
     int32_t C;                // contraction length: K, N, (rows of the expert)
     int32_t NC;               // LIN_DW: columns N
     int32_t n_fblocks;        // ceil(F / 128)
-    int32_t bn;               // most columns of a tile: 16, 32, 64, 128 or 256
+    int32_t bn;               // most columns of a tile: 16, 32, 64, 128, 256 or 320
+    int32_t chunks;           // chunks of the rows when there are no offsets
     int32_t box;              // rows of a TMA box of B (LIN_DW: 64 columns n of each of 64 rows)
     int32_t stages;           // slots of the operand ring
     int32_t ring_bytes;       // its size

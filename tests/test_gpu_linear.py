@@ -84,6 +84,21 @@ def test_linear_forward_few_rows_and_long_sums(T, K, N):
     forward_case(T, K, N, "none", True, True, False, seed=11)
 
 
+# tiles of 256 features shared by two CTAs: rows around their chunks' ends (32,
+# 192, 256 and 320 rows, two accumulators from 257 on), features around 256,
+# contractions around 16 and 64
+@pytest.mark.parametrize("T", [225, 256, 257, 288, 289, 300, 320, 321, 500, 515, 640, 1000])
+def test_linear_forward_pairs(T):
+    forward_case(T, 72, 5128, "gelu", True, True, True, seed=T)
+
+
+@pytest.mark.parametrize("T,K,N", [(129, 8, 9480), (700, 1032, 4104), (2100, 136, 1288), (4099, 200, 520), (1217, 328, 2824)])
+def test_linear_pairs_sizes(T, K, N):
+    forward_case(T, K, N, "none", False, True, False, seed=13)
+    backward_case(T, N, K, "silu", torch.bfloat16, seed=14)
+    backward_case(T, K, N, "relu", torch.float32, seed=15)
+
+
 def test_linear_residual_in_place_and_repeat_calls():
     for T, K, N in ((5, 1024, 512), (700, 256, 520)):
         x, w, r = rnd(1, T, K).cuda(), rnd(2, N, K, std=K ** -0.5).cuda(), rnd(3, T, N).cuda()
@@ -254,6 +269,14 @@ def test_grouped_types_and_rows_of_no_expert(y_dtype, g_dtype):
 
 def test_grouped_wide():
     grouped_case([3, 0, 70, 1, 0, 0, 9, 300], 2056, 1544, seed=6)
+
+
+@pytest.mark.parametrize("counts", [[300, 257, 320, 321, 0, 640, 641, 1000, 31], [960, 961, 1, 0, 512, 288, 289, 1281],
+                                    [256, 0, 255, 225, 224, 193, 192, 161, 700]])
+@pytest.mark.parametrize("K,N", [(72, 2056), (1544, 264)])
+def test_grouped_pairs(counts, K, N):
+    grouped_case(counts, K, N, before=3, after=9, seed=len(counts))
+    grouped_case(counts, K, N, torch.float32, torch.float32, seed=len(counts))
 
 
 def test_grouped_neighbours_do_not_leak():
