@@ -51,14 +51,17 @@
 //
 // Warps: 0 TMA producer, 1 MMA issuer, 2 slot hand-over (LIN_DW: zeroes rows;
 // LIN_PAIR: tells the MMA issuer's CTA that its own half has landed), 3
-// tensor-memory allocation, 4-11 epilogue.  The single threads of warps 0 and 1
+// tensor-memory allocation and tile scheduler, 4-11 epilogue.  The scheduler
+// works out the tiles after a CTA's first, some 700 cycles of divisions and
+// searches each, ahead of the other warps: loads and MMAs of full tiles take the
+// same time, so what either loses between tiles is not made up again.  The single threads of warps 0 and 1
 // are picked by elect.sync and run their loops alone: under `lane == 0` a step's
 // three loads took 708 cycles to issue, against the MMAs' 512, and with loops
 // run by the whole warp on shuffled (uniform) values a step of loads and MMAs
 // took 710; this way it takes 530.
 #include <cuda.h>
 
-#include <climits>
+#include <cstdint>
 #include <type_traits>
 
 #include "activation.cuh"
@@ -70,6 +73,7 @@ namespace moe {
 constexpr int LN_THREADS = 384;
 constexpr int LN_EPI_WARPS = 8, LN_EPI_THREADS = 32 * LN_EPI_WARPS;
 constexpr int LN_MAX_STAGES = 10;
+constexpr int LN_TILES = 4;               // tiles scheduled ahead
 constexpr int LN_ACCS = 4;                // accumulators in use at a time
 constexpr int LN_SUB = 192;               // columns of the first accumulator of a tile of more than 256
 constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
@@ -85,6 +89,12 @@ static __device__ int32_t g_linear_status;
 // contraction, or two CTAs per tile of 256 features.
 enum LinShare { LIN_ONE, LIN_SPLIT, LIN_PAIR };
 
+struct alignas(16) Tile {
+    int e, f0;            // expert (-1: there is no tile), the CTA's first feature
+    int col0, ncols;      // output rows (LIN_FWD, LIN_DX: rows; LIN_DW: n) of the tile
+    int c0, k0, k1, clen; // contraction: first row (LIN_DW), steps [k0, k1), length
+};
+
 struct LinSmem {
     uint64_t full[LN_MAX_STAGES];    // TMA data of the slot landed (tx counted)
     uint64_t empty[LN_MAX_STAGES];   // the slot's MMAs completed
@@ -92,6 +102,9 @@ struct LinSmem {
     uint64_t drained;                // all MMAs of this CTA (pair) completed
     uint64_t acc_full[LN_ACCS];      // accumulator holds a finished tile
     uint64_t acc_empty[LN_ACCS];     // epilogue (of both CTAs) finished reading the accumulator
+    uint64_t tile_full[LN_TILES];    // the scheduler wrote the tile
+    uint64_t tile_empty[LN_TILES];   // all that use it have read it
+    Tile tiles[LN_TILES];
     uint32_t tmem_base;
     int32_t status;                  // of this CTA; joined into g_linear_status at the end
     int32_t first[LN_MAX_E + 1];     // chunks before each expert (LIN_FWD, LIN_DX)
@@ -112,12 +125,6 @@ static_assert(2 * (1024 + 1024 + LN_HALF_RING_BYTES + LN_STG_OFFSET) <= 233472, 
 __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
-
-struct Tile {
-    int e, f0;            // the CTA's first feature
-    int col0, ncols;      // output rows (LIN_FWD, LIN_DX: rows; LIN_DW: n) of the tile
-    int c0, k0, k1, clen; // contraction: first row (LIN_DW), steps [k0, k1), length
-};
 
 // Chunks of an expert's rows.  Tiles of up to 320 rows save a pass over the
 // weights where few chunks of up to 256 would be narrow.
@@ -345,6 +352,10 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             mbar_init(&sm->full[lane], 1);
             mbar_init(&sm->empty[lane], 1);
             mbar_init(&sm->ready[lane], PAIR ? 2 : 1);
+            if (lane < LN_TILES) {   // read by warps 0, 1 (where it issues), 2 (where it hands over) and the epilogue's
+                mbar_init(&sm->tile_full[lane], 1);
+                mbar_init(&sm->tile_empty[lane], 1 + leader + HAND_OVER + LN_EPI_WARPS);
+            }
         } else if (lane < LN_MAX_STAGES + LN_ACCS) {
             mbar_init(&sm->acc_full[lane - LN_MAX_STAGES], 1);
             mbar_init(&sm->acc_empty[lane - LN_MAX_STAGES], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
@@ -405,7 +416,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
     const int n_tiles = n_units * p.n_fblocks;
     const int tile0 = SPLIT ? int(blockIdx.x) / p.split : PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
-    const int tstep = SPLIT ? INT_MAX / 2 : PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
+    const int tstep = PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
     // the accumulators of a tile: MMA's N, and the rows of B (the columns of D)
     // that this CTA loads
     constexpr bool WIDE = PAIR && MODE != LIN_DW;
@@ -415,17 +426,26 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     auto b_rows = [&](int ncols) { return PAIR ? mma_n(ncols) / 2 : ncols; };
     auto b_boxes = [&](int ncols) { return (b_rows(ncols) + p.box - 1) / p.box; };
 
-    int tile = tile0;
-    Tile t = {};
-    if (tile < n_tiles) t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
-    auto advance = [&] {
-        tile += tstep;
-        if (tile < n_tiles) t = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+    // the CTA's first tile is worked out by every warp, the others come from the scheduler
+    Tile t = {-1};
+    if (tile0 < n_tiles) t = get_tile<MODE, SHARE>(tile0, sm, p, n_units, rank);
+    uint32_t tiles_read = 0;
+    auto advance = [&](bool whole_warp) {
+        if (SPLIT) {
+            t.e = -1;
+            return;
+        }
+        const uint32_t i = tiles_read % LN_TILES;
+        if (mbar_wait(&sm->tile_full[i], (tiles_read / LN_TILES) & 1, &sm->status)) t = sm->tiles[i];
+        else t.e = -1;
+        ++tiles_read;
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(&sm->tile_empty[i]);
     };
 
     uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;   // SPLIT: this thread's pieces of them
     if (!p.offsets) {
-        if (MODE != LIN_DW && warp == 0 && tile < n_tiles && elect_one()) {
+        if (MODE != LIN_DW && warp == 0 && t.e >= 0 && elect_one()) {
             for (int kk = t.k0; kk < t.k1 && kk < t.k0 + p.stages; ++kk) {
                 if (MODE == LIN_FWD) {
                     tma_prefetch_3d(&tm_a, kk * 64, t.f0, t.e);
@@ -444,7 +464,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         if (elect_one()) {
             uint32_t slot = 0, par = 1, filled = 0;
             bool ok = true;
-            for (; tile < n_tiles && ok; advance()) {
+            for (; t.e >= 0 && ok; advance(false)) {
                 const int n0 = sub_cols(t, 0), n1 = subs(t) > 1 ? t.ncols - n0 : 0;
                 const int boxes0 = b_boxes(n0), boxes = boxes0 + (WIDE ? b_boxes(n1) : 0);
                 const int row = t.col0 + (PAIR ? int(rank) * b_rows(n0) : 0);
@@ -532,7 +552,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 }
                 return true;
             };
-            for (; tile < n_tiles && ok; advance()) {
+            for (; t.e >= 0 && ok; advance(false)) {
                 if (t.k0 >= t.k1) continue;   // nothing to contract: the epilogue writes zeros
                 const int n0 = mma_n(sub_cols(t, 0)), n1 = subs(t) > 1 ? mma_n(sub_cols(t, 1)) : 0;
                 const uint32_t idesc0 = idesc_m | uint32_t(n0 >> 3) << 17, idesc1 = idesc_m | uint32_t(n1 >> 3) << 17;
@@ -555,7 +575,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         // ---------------- hand the slots over to the MMA issuer ----------------
         uint32_t slot = 0, par = 0;
         bool ok = true;
-        for (; tile < n_tiles && ok; advance()) {
+        for (; t.e >= 0 && ok; advance(true)) {
             const int boxes = b_boxes(t.ncols);   // LIN_DW
             for (int kk = t.k0; kk < t.k1; ++kk) {
                 if (!mbar_wait(&sm->full[slot], par, &sm->status)) { ok = false; break; }
@@ -581,13 +601,26 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
             }
         }
+    } else if (warp == 3 && !SPLIT) {
+        // ------------------------------ tile scheduler ------------------------------
+        if (lane == 0 && tile0 < n_tiles) {
+            int tile = tile0;
+            for (uint32_t i = 0; tile < n_tiles; ++i) {
+                tile += tstep;
+                Tile next = {-1};
+                if (tile < n_tiles) next = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+                if (!mbar_wait(&sm->tile_empty[i % LN_TILES], ((i / LN_TILES) & 1) ^ 1, &sm->status)) break;
+                sm->tiles[i % LN_TILES] = next;
+                mbar_arrive(&sm->tile_full[i % LN_TILES]);
+            }
+        }
     } else if (warp >= 4) {
         // ------------------------------ epilogue ------------------------------
         const int ew = warp & 3;                 // TMEM lanes 32 ew .. 32 ew + 31
         const uint32_t stage = smem_u32(sm) + LN_STG_OFFSET + (warp - 4) * LN_STG_BYTES;
         uint32_t n = 0;
         AccColumns cols;
-        for (bool ok = true; tile < n_tiles && ok; advance()) {
+        for (bool ok = true; t.e >= 0 && ok; advance(true)) {
             const bool any = t.k0 < t.k1;
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             if (SPLIT && MODE == LIN_FWD) {   // under the sums: what the end of the tile reads besides them
@@ -661,7 +694,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         __syncwarp();
         if (p.split > 1) cluster_sync();
         else __syncthreads();
-        if (warp >= 4 && tile < n_tiles) {
+        if (warp >= 4 && t.e >= 0) {
             // 16 threads to a column, each with eight features
             const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             const int f8 = 8 * (threadIdx.x & 15), f = t.f0 + f8, step = p.split * (LN_EPI_THREADS / 16);
