@@ -332,6 +332,21 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of the cluster barrier; arriving orders no memory accesses.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// 16 bytes to the shared memory of another CTA of this cluster, at the offset that
+// `addr` has in this one, counted on the barrier at `bar`'s offset there.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t rank, uint64_t* bar, uint32_t x, uint32_t y,
+                                            uint32_t z, uint32_t w) {
+    asm volatile("{\n\t.reg .b32 a, b;\n\t"
+                 "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+                 "mapa.shared::cluster.u32 b, %1, %2;\n\t"
+                 "st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [a], {%3, %4, %5, %6}, [b];\n\t}"
+                 :: "r"(addr), "r"(smem_u32(bar)), "r"(rank), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
 // A float in the shared memory of CTA `rank` of this cluster, at the address
 // `p` has in this CTA.
 __device__ __forceinline__ float ld_dsmem_f32(const float* p, uint32_t rank) {

@@ -38,9 +38,11 @@
 // scan over the (at most 256) experts.
 //
 // LIN_SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
-// shares one tile's contraction.  Each leaves its partial sums in its shared
-// memory, and the CTAs add each other's through distributed shared memory in
-// rank order: no scratch, no atomics, the same bits every time.  Such calls are
+// shares one tile's contraction, and each finishes a part of the tile: partial
+// sums are added in rank order through distributed shared memory -- no scratch,
+// no atomics, the same bits every time.  Those of tiles of up to 64 columns are
+// sent to the CTA that finishes them (st.async, counted by a barrier there);
+// those of wider ones stay in their CTA's ring, to be read from there.  Short calls are
 // short and bound by the weights' bytes, so what counts is how soon a call's
 // loads follow the last call's: tiles of up to 64 columns take half of an SM's
 // shared memory and 64 columns of tensor memory, so that the next call's CTAs
@@ -79,7 +81,7 @@ constexpr int LN_SUB = 192;               // columns of the first accumulator of
 constexpr int LN_MAX_E = 256;             // one thread per expert in the scan
 constexpr int LN_A_BYTES = 128 * 64 * 2;  // 16 KB
 constexpr int LN_RING_BYTES = 196608;     // the ring of a CTA that has an SM to itself
-constexpr int LN_HALF_RING_BYTES = 106496;   // of one that shares it with another
+constexpr int LN_HALF_RING_BYTES = 109568;   // of one that shares it with another, with the sums it is sent
 constexpr int LN_STG_BYTES = 32 * 64;     // an epilogue warp's staging buffer: 32 columns x 32 features, bf16
 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
@@ -102,6 +104,7 @@ struct LinSmem {
     uint64_t drained;                // all MMAs of this CTA (pair) completed
     uint64_t acc_full[LN_ACCS];      // accumulator holds a finished tile
     uint64_t acc_empty[LN_ACCS];     // epilogue (of both CTAs) finished reading the accumulator
+    uint64_t sums_full;              // LIN_SPLIT: all partial sums that are sent here have landed
     uint64_t tile_full[LN_TILES];    // the scheduler wrote the tile
     uint64_t tile_empty[LN_TILES];   // all that use it have read it
     Tile tiles[LN_TILES];
@@ -361,6 +364,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             mbar_init(&sm->acc_empty[lane - LN_MAX_STAGES], PAIR ? 2 * LN_EPI_WARPS : LN_EPI_WARPS);
         } else if (lane == LN_MAX_STAGES + LN_ACCS) {
             mbar_init(&sm->drained, 1);
+            mbar_init(&sm->sums_full, 1 + LN_EPI_WARPS);   // the bytes that others send; this CTA's own epilogue warps
             sm->status = DEV_OK;
         } else if (lane == LN_MAX_STAGES + LN_ACCS + 1) {
             prefetch_tmap(&tm_a);
@@ -410,7 +414,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     }
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_sync();   // the peer's barriers are initialized, both allocations done
+    // the other CTAs' barriers are initialized (a pair's allocations done)
+    if (PAIR || (SPLIT && p.split > 1)) cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sm->tmem_base;
     const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
@@ -443,7 +448,24 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         if (!whole_warp || lane == 0) mbar_arrive(&sm->tile_empty[i]);
     };
 
-    uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;   // SPLIT: this thread's pieces of them
+    auto out_row = [&](const Tile& t) { return MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : int64_t(t.col0); };
+
+    // SPLIT: a unit is eight features and four columns of the tile; each CTA
+    // finishes `units` of them in a row (the last ones fewer).  Sent sums lie in
+    // [sender][unit][feature, turned by the unit][4 columns]: 16-byte pieces that
+    // the eight units a warp reads at a time have in different banks.
+    const bool sent = p.bn <= 64;
+    const int64_t split_row = SPLIT ? out_row(t) : 0;
+    const int n_sums = (t.ncols + 3) / 4 * 16, units = (n_sums + p.split - 1) / p.split;
+    const int my_units = max(0, min(units, n_sums - int(rank) * units));
+    unsigned char* sums_at = p.split > 1 ? reinterpret_cast<unsigned char*>(sm) + LN_STG_OFFSET : base;
+    uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;
+    auto load_ends = [&](int i) {   // bias and residual of piece i
+        const int u = rank * units + (i >> 2), col = 4 * (u >> 4) + (i & 3), f = t.f0 + 8 * (u & 15);
+        if (MODE != LIN_FWD || i >= 4 * my_units || col >= t.ncols || f >= p.F) return;
+        if (p.bias) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
+        if (p.residual) res0 = *reinterpret_cast<const uint4*>(p.residual + (split_row + col) * p.F + f);
+    };
     if (!p.offsets) {
         if (MODE != LIN_DW && warp == 0 && t.e >= 0 && elect_one()) {
             for (int kk = t.k0; kk < t.k1 && kk < t.k0 + p.stages; ++kk) {
@@ -622,14 +644,46 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         AccColumns cols;
         for (bool ok = true; t.e >= 0 && ok; advance(true)) {
             const bool any = t.k0 < t.k1;
-            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
-            if (SPLIT && MODE == LIN_FWD) {   // under the sums: what the end of the tile reads besides them
-                const int f = t.f0 + 8 * (threadIdx.x & 15), col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16;
-                if (p.bias && f < p.F) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
-                if (p.residual && f < p.F && col < t.ncols)
-                    res0 = *reinterpret_cast<const uint4*>(p.residual + (row0 + col) * p.F + f);
+            const int64_t row0 = out_row(t);
+            if (SPLIT && sent) {
+                if (threadIdx.x == 128) mbar_arrive_expect_tx(&sm->sums_full, (p.split - 1) * my_units * 128);
+                load_ends(threadIdx.x - 128);   // under the sums: what the end of the tile reads besides them
+                bool got = any;
+                if (any) {
+                    got = mbar_wait(&sm->acc_full[0], 0, &sm->status);
+                    tc_fence_after();
+                }
+                // 16-byte pieces of one feature and four columns, also after a
+                // wait that gave up: the others count on them
+                const uint32_t sums = smem_u32(sums_at);
+                for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
+                    uint32_t v[32];
+                    if (got) {
+                        tmem_ld32(tmem + (uint32_t(32 * ew) << 16) + cc * 32, v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0u;
+                    }
+                    const int u = cc * 128 + 4 * ew + (lane >> 3);
+                    int owner = u / units, at = u - owner * units;
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) {
+                        if (cc * 32 + 4 * g < t.ncols) {
+                            const uint32_t to = sums + ((rank * units + at) * 8 + ((lane + at) & 7)) * 16;
+                            if (owner == int(rank))
+                                st_shared_v4_at(to, make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
+                            else
+                                st_async_v4(to, owner, &sm->sums_full, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+                        }
+                        at += 16;
+                        while (at >= units) { at -= units; ++owner; }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->sums_full);
+                break;     // a split tile is its cluster's only one
             }
-            if (SPLIT) {   // partial sums [col][128], added up below
+            if (SPLIT) {   // partial sums [col][128], read by the others below
                 if (any) {
                     if (!mbar_wait(&sm->acc_full[0], 0, &sm->status)) break;
                     tc_fence_after();
@@ -647,7 +701,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     for (int j = 0; j < 32; ++j)
                         if (cc * 32 + j < t.ncols) red[j * 128] = __uint_as_float(v[j]);
                 }
-                break;     // a split tile is its cluster's only one
+                break;
             }
             for (int sub = 0; sub < subs(t); ++sub) {
                 const int ncols = sub_cols(t, sub);
@@ -689,21 +743,41 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             }
         }
     }
-    if (SPLIT) {
+    if (SPLIT && sent) {
+        __syncwarp();
+        if (p.split > 1) cluster_arrive();       // this CTA has sent what it sends
+        bool ok = true;
+        if (warp >= 4 && t.e >= 0) {
+            ok = mbar_wait(&sm->sums_full, 0, &sm->status);
+            // a thread has eight features of one column
+            for (int i = threadIdx.x - 128; i < 4 * my_units; i += LN_EPI_THREADS) {
+                const int at = i >> 2, u = rank * units + at, col = 4 * (u >> 4) + (i & 3), f = t.f0 + 8 * (u & 15);
+                if (i >= LN_EPI_THREADS) load_ends(i);
+                const float* q = reinterpret_cast<const float*>(sums_at) + at * 32 + (i & 3);
+                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                for (int s = 0; s < p.split; ++s)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += q[s * units * 32 + ((j + at) & 7) * 4];
+                if (col < t.ncols && f < p.F) finish8<MODE>(p, (split_row + col) * p.F + f, v, bias0, res0);
+            }
+        }
+        __syncwarp();
+        if (p.split > 1) cluster_wait();
+        // a wait that gave up: all has been sent, and lands before this CTA leaves
+        if (!ok) mbar_wait(&sm->sums_full, 0, nullptr);
+    } else if (SPLIT) {
         // every CTA's partial sums are in its shared memory
         __syncwarp();
         if (p.split > 1) cluster_sync();
         else __syncthreads();
         if (warp >= 4 && t.e >= 0) {
             // 16 threads to a column, each with eight features
-            const int64_t row0 = MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : t.col0;
             const int f8 = 8 * (threadIdx.x & 15), f = t.f0 + f8, step = p.split * (LN_EPI_THREADS / 16);
             const float* red = reinterpret_cast<const float*>(base) + f8;
             for (int col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16; col < t.ncols && f < p.F; col += step) {
-                const int64_t idx = (row0 + col) * p.F + f;
-                const uint4 res = res0;
-                if (MODE == LIN_FWD && p.residual && col + step < t.ncols)
-                    res0 = *reinterpret_cast<const uint4*>(p.residual + idx + int64_t(step) * p.F);
+                const int64_t idx = (split_row + col) * p.F + f;
+                if (MODE == LIN_FWD && p.residual) res0 = *reinterpret_cast<const uint4*>(p.residual + idx);
+                if (MODE == LIN_FWD && p.bias) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
                 float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 4
                 for (int s = 0; s < p.split; ++s) {
@@ -712,7 +786,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
                     v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
                 }
-                finish8<MODE>(p, idx, v, bias0, res);
+                finish8<MODE>(p, idx, v, bias0, res0);
             }
         }
         __syncwarp();
@@ -892,13 +966,13 @@ int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
 }
 
 template <int MODE>
-moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int share, int64_t tiles,
-                       int sms, cudaStream_t stream) {
+moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int share, int sums,
+                       int64_t tiles, int sms, cudaStream_t stream) {
     auto kernel = share == LIN_PAIR    ? linear_kernel<MODE, LIN_PAIR>
                   : share == LIN_SPLIT ? linear_kernel<MODE, LIN_SPLIT>
                                        : linear_kernel<MODE, LIN_ONE>;
     if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
-    const size_t smem = 1024 + p.ring_bytes + LN_STG_OFFSET + (share == LIN_SPLIT ? 0 : LN_EPI_WARPS * LN_STG_BYTES);
+    const size_t smem = 1024 + p.ring_bytes + LN_STG_OFFSET + (share == LIN_SPLIT ? sums : LN_EPI_WARPS * LN_STG_BYTES);
     const int64_t cluster = share == LIN_PAIR ? 2 : share == LIN_SPLIT ? p.split : 1;
     const int64_t grid = share == LIN_SPLIT ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
     return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, smem, unsigned(cluster), stream, ta, tb, p);
@@ -954,19 +1028,21 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
     p.box = mode == LIN_DW ? 64 : share == LIN_PAIR ? 32 : p.bn < 64 ? p.bn : 64;
     const int stage = LN_A_BYTES + (share == LIN_PAIR ? p.bn / 2 : p.bn) * 128;
     const bool half = share == LIN_SPLIT && p.bn <= 64;
-    p.stages = (half ? LN_HALF_RING_BYTES : LN_RING_BYTES) / stage;
+    const int sums = half && p.split > 1 ? p.split * int(ceil_div(4 * p.bn, p.split)) * 128 : 0;
+    p.stages = (half ? LN_HALF_RING_BYTES - sums : LN_RING_BYTES) / stage;
     if (p.stages > LN_MAX_STAGES) p.stages = LN_MAX_STAGES;
     p.ring_bytes = p.stages * stage;
-    if (share == LIN_SPLIT && p.ring_bytes < p.bn * 512) p.ring_bytes = p.bn * 512;   // its partial sums reuse the ring
+    // the partial sums of a tile that is not split, or is wide, reuse the ring
+    if (share == LIN_SPLIT && !sums && p.ring_bytes < p.bn * 512) p.ring_bytes = p.bn * 512;
     p.tmem_cols = share == LIN_SPLIT ? (p.bn < 32 ? 32 : p.bn) : 512;
     CUtensorMap ta, tb;
     const bool ok = mode == LIN_DW
         ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
         : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, p.box);
     if (!ok) return MOE_ERR_CUDA;
-    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
-    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
-    return launch_mode<LIN_DW>(ta, tb, p, share, n_units * p.n_fblocks, sms, stream);
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
+    return launch_mode<LIN_DW>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
 }
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
