@@ -752,13 +752,14 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             // a thread has eight features of one column
             for (int i = threadIdx.x - 128; i < 4 * my_units; i += LN_EPI_THREADS) {
                 const int at = i >> 2, u = rank * units + at, col = 4 * (u >> 4) + (i & 3), f = t.f0 + 8 * (u & 15);
-                if (i >= LN_EPI_THREADS) load_ends(i);
+                const uint4 bias = bias0, res = res0;
+                load_ends(i + LN_EPI_THREADS);   // of the next piece, under this one's sums
                 const float* q = reinterpret_cast<const float*>(sums_at) + at * 32 + (i & 3);
                 float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 for (int s = 0; s < p.split; ++s)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] += q[s * units * 32 + ((j + at) & 7) * 4];
-                if (col < t.ncols && f < p.F) finish8<MODE>(p, (split_row + col) * p.F + f, v, bias0, res0);
+                if (col < t.ncols && f < p.F) finish8<MODE>(p, (split_row + col) * p.F + f, v, bias, res);
             }
         }
         __syncwarp();
