@@ -149,27 +149,19 @@ struct AccColumns {
 };
 
 template <int MODE, int SHARE>
-__device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinParams& p, int n_units, int rank) {
-    // feature blocks in groups of 2048 features, unit by unit within a group:
-    // the concurrent tiles of 148 CTAs then share 2048 features and 9 row
-    // chunks in L2
+__device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinParams& p, int rank) {
+    // Expert by expert, so that its rows are in L2 for all of their tiles; within
+    // an expert feature blocks in groups of 2048 features, chunk by chunk within a
+    // group: the concurrent tiles of 148 CTAs then share 2048 features and 9 row
+    // chunks.
     constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
-    const int gf = min(PAIR ? 8 : 16, p.n_fblocks);
-    const int n_groups = (p.n_fblocks + gf - 1) / gf;
-    const int g = min(tile / (n_units * gf), n_groups - 1);
-    const int r = tile - g * n_units * gf;
-    const int gsize = min(gf, p.n_fblocks - g * gf);
-    const int unit = r / gsize;
     Tile t;
-    const int fb = g * gf + (r - unit * gsize);
-    t.f0 = 128 * (PAIR ? 2 * fb + rank : fb);
+    int n, before;                         // the expert's chunks (LIN_DW: column blocks), those before it
+    const int unit = tile / p.n_fblocks;   // not the tile's chunk, but one of its expert's
     if (MODE == LIN_DW) {
-        const int ncb = (p.NC + p.bn - 1) / p.bn;
-        t.e = unit / ncb;
-        t.col0 = (unit - t.e * ncb) * p.bn;
-        t.ncols = min(p.bn, p.NC - t.col0);
-        t.c0 = sm->begin[t.e];
-        t.clen = sm->count[t.e];
+        n = (p.NC + p.bn - 1) / p.bn;
+        t.e = unit / n;
+        before = t.e * n;
     } else {
         int lo = 0, hi = p.E;              // the last expert whose first chunk is <= unit
         while (hi - lo > 1) {
@@ -177,12 +169,24 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
             if (sm->first[mid] <= unit) lo = mid; else hi = mid;
         }
         t.e = lo;
-        const int chunks = sm->first[lo + 1] - sm->first[lo], cnt = sm->count[lo];
+        before = sm->first[lo];
+        n = sm->first[lo + 1] - before;
+    }
+    const int gf = min(PAIR ? 8 : 16, p.n_fblocks);
+    const int in_e = tile - before * p.n_fblocks, g = in_e / (n * gf), r = in_e - g * n * gf;
+    const int gsize = min(gf, p.n_fblocks - g * gf), i = r / gsize, fb = g * gf + (r - i * gsize);
+    t.f0 = 128 * (PAIR ? 2 * fb + rank : fb);
+    if (MODE == LIN_DW) {
+        t.col0 = i * p.bn;
+        t.ncols = min(p.bn, p.NC - t.col0);
+        t.c0 = sm->begin[t.e];
+        t.clen = sm->count[t.e];
+    } else {
+        const int cnt = sm->count[t.e];
         const int align = PAIR ? 31 : 15;   // of the MMA's N
-        const int size = ((cnt + chunks - 1) / chunks + align) & ~align;
-        const int i = unit - sm->first[lo];
-        t.col0 = sm->begin[lo] + i * size;
-        t.ncols = max(0, min(size, cnt - i * size));
+        const int size = ((cnt + n - 1) / n + align) & ~align;
+        t.col0 = sm->begin[t.e] + i * size;
+        t.ncols = min(size, cnt - i * size);
         t.c0 = 0;
         t.clen = p.C;
     }
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
 
     // the CTA's first tile is worked out by every warp, the others come from the scheduler
     Tile t = {-1};
-    if (tile0 < n_tiles) t = get_tile<MODE, SHARE>(tile0, sm, p, n_units, rank);
+    if (tile0 < n_tiles) t = get_tile<MODE, SHARE>(tile0, sm, p, rank);
     uint32_t tiles_read = 0;
     auto advance = [&](bool whole_warp) {
         if (SPLIT) {
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             for (uint32_t i = 0; tile < n_tiles; ++i) {
                 tile += tstep;
                 Tile next = {-1};
-                if (tile < n_tiles) next = get_tile<MODE, SHARE>(tile, sm, p, n_units, rank);
+                if (tile < n_tiles) next = get_tile<MODE, SHARE>(tile, sm, p, rank);
                 if (!mbar_wait(&sm->tile_empty[i % LN_TILES], ((i / LN_TILES) & 1) ^ 1, &sm->status)) break;
                 sm->tiles[i % LN_TILES] = next;
                 mbar_arrive(&sm->tile_full[i % LN_TILES]);
