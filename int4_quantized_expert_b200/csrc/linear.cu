@@ -261,12 +261,13 @@ __device__ __forceinline__ void finish_block(const LinParams& p, float (&a)[2][1
             st_matrix4_t(mat + 512 * i, m);
         }
         __syncwarp();
+        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 v = ld_shared_v4_at(piece + 512 * i);
-            if (fok && 8 * i + rl < ncols) *reinterpret_cast<uint4*>(out + (row + 8 * i + rl) * p.F + f) = v;
-        }
+        for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4_at(piece + 512 * i);
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (fok && 8 * i + rl < ncols) *reinterpret_cast<uint4*>(out + (row + 8 * i + rl) * p.F + f) = v[i];
     };
     uint4 res[4];
     if (MODE == LIN_FWD) {
@@ -816,29 +817,31 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
 // dz = dy * act'(z) and dbias = sum over the rows of dz (unrounded)
 //
 // HBM-bound: dy and z are read once, dz is written once, the column sums ride
-// along.  A cluster of AG_SPLIT CTAs takes a strip of 64 columns: 8 threads x
-// 16 bytes a row (one 128-byte line), 32 rows at a time, each CTA a part of
-// the rows.  A thread sums its rows in fp32, the CTA its 32 row lanes and the
-// cluster its CTAs in a fixed order.
+// along.  A cluster of AG_SPLIT CTAs takes a strip of AG_COLS columns: 8 threads
+// x 16 bytes a row (one 128-byte line), 32 rows at a time, each CTA a part of
+// the rows.  A thread sums its rows in fp32, the CTA its row lanes and the
+// cluster its CTAs in a fixed order.  4099 x 5120 with GELU: 24 us, 5.2 TB/s;
+// strips of 32 and 128 columns, 512 threads and two or eight rows in flight a
+// thread all took 28 to 37 us.
 // ---------------------------------------------------------------------------
-constexpr int AG_THREADS = 256, AG_SPLIT = 8;
+constexpr int AG_THREADS = 256, AG_SPLIT = 8, AG_COLS = 64, AG_ROWS = AG_THREADS * 8 / AG_COLS;
 
 template <bool DZ, bool DB>
 __global__ void __launch_bounds__(AG_THREADS) act_grad_kernel(const bf16* __restrict__ dy, const bf16* __restrict__ z,
                                                               int T, int N, int act, bf16* __restrict__ dz,
                                                               void* __restrict__ dbias, int dbias_fp32) {
-    __shared__ float part[32][65];
-    __shared__ float sums[64];
+    __shared__ float part[AG_ROWS][AG_COLS + 1];
+    __shared__ float sums[AG_COLS];
     griddep_launch_dependents();
     griddep_wait();
-    const int split = blockIdx.x % AG_SPLIT, n0 = int(blockIdx.x / AG_SPLIT) * 64;
-    const int c8 = threadIdx.x & 7, rl = threadIdx.x >> 3;
+    const int split = blockIdx.x % AG_SPLIT, n0 = int(blockIdx.x / AG_SPLIT) * AG_COLS;
+    const int c8 = threadIdx.x % (AG_COLS / 8), rl = threadIdx.x / (AG_COLS / 8);
     const int col = n0 + 8 * c8;
     const int r0 = int(int64_t(T) * split / AG_SPLIT), r1 = int(int64_t(T) * (split + 1) / AG_SPLIT);
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (col < N) {   // N is a multiple of 8
 #pragma unroll 4
-        for (int r = r0 + rl; r < r1; r += 32) {
+        for (int r = r0 + rl; r < r1; r += AG_ROWS) {
             const int64_t idx = int64_t(r) * N + col;
             float v[8];
             unpack8(*reinterpret_cast<const uint4*>(dy + idx), v);
@@ -857,14 +860,14 @@ __global__ void __launch_bounds__(AG_THREADS) act_grad_kernel(const bf16* __rest
 #pragma unroll
     for (int i = 0; i < 8; ++i) part[rl][8 * c8 + i] = s[i];
     __syncthreads();
-    if (threadIdx.x < 64) {
+    if (threadIdx.x < AG_COLS) {
         float t = 0.0f;
-        for (int i = 0; i < 32; ++i) t += part[i][threadIdx.x];
+        for (int i = 0; i < AG_ROWS; ++i) t += part[i][threadIdx.x];
         sums[threadIdx.x] = t;
     }
     cluster_sync();
     const int n = n0 + int(threadIdx.x);
-    if (split == 0 && threadIdx.x < 64 && n < N) {
+    if (split == 0 && threadIdx.x < AG_COLS && n < N) {
         float t = 0.0f;
         for (int i = 0; i < AG_SPLIT; ++i) t += ld_dsmem_f32(&sums[threadIdx.x], i);
         if (dbias_fp32) static_cast<float*>(dbias)[n] = t;
@@ -1052,7 +1055,7 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
                            int32_t dbias_fp32, cudaStream_t stream) {
-    const unsigned grid = unsigned(ceil_div(N, 64) * AG_SPLIT);
+    const unsigned grid = unsigned(ceil_div(N, AG_COLS) * AG_SPLIT);
     if (z && dbias)
         return launch_cluster(act_grad_kernel<true, true>, grid, AG_THREADS, 0, AG_SPLIT, stream, dy, z, T, N, act, dz,
                               dbias, dbias_fp32);
