@@ -37,16 +37,15 @@
 // cycle that an SM can load are what bounds narrow tiles.  Each CTA derives the list from the offsets by a
 // scan over the (at most 256) experts.
 //
-// LIN_SPLIT: when there are far fewer tiles than SMs, a cluster of up to 8 CTAs
-// shares one tile's contraction, and each finishes a part of the tile: partial
-// sums are added in rank order through distributed shared memory -- no scratch,
-// no atomics, the same bits every time.  Those of tiles of up to 64 columns are
-// sent to the CTA that finishes them (st.async, counted by a barrier there);
-// those of wider ones stay in their CTA's ring, to be read from there.  Short calls are
-// short and bound by the weights' bytes, so what counts is how soon a call's
-// loads follow the last call's: tiles of up to 64 columns take half of an SM's
-// shared memory and 64 columns of tensor memory, so that the next call's CTAs
-// (programmatic dependent launch) are set up and waiting beside this one's.
+// LIN_SPLIT: when the tiles fit the SMs at once, a CTA takes one tile of up to
+// 128 columns, or a cluster of up to 8 CTAs shares one tile's contraction and each
+// finishes a part of the tile.  Partial sums are sent to the CTA that finishes
+// them (st.async to its shared memory, counted by a barrier there) and added in
+// rank order: no scratch, no atomics, the same bits every time.  Short calls are
+// bound by latency or by the weights' bytes, so what counts is how soon a call's
+// loads follow the last call's: where half of an SM's shared memory is enough, the
+// next call's CTAs (programmatic dependent launch) are set up and waiting beside
+// this one's.
 //
 // Without offsets, a CTA knows its weights before it has waited for the kernel
 // before it, and asks for a ring's worth of them to be brought into L2.
@@ -56,14 +55,16 @@
 // tensor-memory allocation and tile scheduler, 4-11 epilogue.  The scheduler
 // works out the tiles after a CTA's first, some 700 cycles of divisions and
 // searches each, ahead of the other warps: loads and MMAs of full tiles take the
-// same time, so what either loses between tiles is not made up again.  The single threads of warps 0 and 1
-// are picked by elect.sync and run their loops alone: under `lane == 0` a step's
-// three loads took 708 cycles to issue, against the MMAs' 512, and with loops
-// run by the whole warp on shuffled (uniform) values a step of loads and MMAs
-// took 710; this way it takes 530.
+// same time, so what either loses between tiles is not made up again.  The single
+// threads of warps 0 and 1 are picked by elect.sync and run their loops alone:
+// under `lane == 0` a step's three loads took 708 cycles to issue, against the
+// MMAs' 512, and with loops run by the whole warp on shuffled (uniform) values a
+// step of loads and MMAs took 710; this way it takes 530.
 #include <cuda.h>
 
 #include <cstdint>
+#include <map>
+#include <tuple>
 #include <type_traits>
 
 #include "activation.cuh"
@@ -120,6 +121,7 @@ constexpr int LN_STG_OFFSET = (int(sizeof(LinSmem)) + 127) & ~127;
 constexpr int LN_SMEM_BYTES = 1024 + LN_RING_BYTES + LN_STG_OFFSET + LN_EPI_WARPS * LN_STG_BYTES;
 static_assert(LN_SMEM_BYTES <= 232448, "shared memory of a block");
 static_assert(2 * (1024 + 1024 + LN_HALF_RING_BYTES + LN_STG_OFFSET) <= 233472, "two blocks on an SM");
+constexpr int LN_FULL_RING_BYTES = 232448 - 1024 - LN_STG_OFFSET;   // of a split tile's CTA that has an SM to itself
 
 // Shared-memory matrix descriptor of an MN-major tile with the 128-byte
 // swizzle: rows of 64 values along M or N (128 bytes), one per c; 8 c are
@@ -329,15 +331,6 @@ __device__ __forceinline__ void finish_block(const LinParams& p, float (&a)[2][1
             }
 }
 
-__device__ __forceinline__ float4 ld_dsmem_f32x4(const float* p, uint32_t rank) {
-    uint32_t remote;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(p)), "r"(rank));
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(remote) : "memory");
-    return v;
-}
-
 template <int MODE, int SHARE>
 __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear_kernel(const __grid_constant__ CUtensorMap tm_a,
                                                                const __grid_constant__ CUtensorMap tm_b, LinParams p) {
@@ -456,20 +449,23 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     auto out_row = [&](const Tile& t) { return MODE == LIN_DW ? int64_t(t.e) * p.NC + t.col0 : int64_t(t.col0); };
 
     // SPLIT: a unit is eight features and four columns of the tile; each CTA
-    // finishes `units` of them in a row (the last ones fewer).  Sent sums lie in
+    // finishes `units` of them in a row (the last ones fewer).  Sums lie in
     // [sender][unit][feature, turned by the unit][4 columns]: 16-byte pieces that
     // the eight units a warp reads at a time have in different banks.
-    const bool sent = p.bn <= 64;
     const int64_t split_row = SPLIT ? out_row(t) : 0;
     const int n_sums = (t.ncols + 3) / 4 * 16, units = (n_sums + p.split - 1) / p.split;
     const int my_units = max(0, min(units, n_sums - int(rank) * units));
     unsigned char* sums_at = p.split > 1 ? reinterpret_cast<unsigned char*>(sm) + LN_STG_OFFSET : base;
+    // A thread finishes eight features of a column at a time, LN_EPI_THREADS / 4
+    // units apart: its features stay the same.  The bias and the first residual are
+    // loaded under the sums, each next residual under the piece before.
+    const int i0 = int(threadIdx.x) - 128;
+    const int split_f = t.f0 + 8 * ((int(rank) * units + (i0 >> 2)) & 15);
+    auto split_col = [&](int i) { return 4 * ((int(rank) * units + (i >> 2)) >> 4) + (i & 3); };
     uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;
-    auto load_ends = [&](int i) {   // bias and residual of piece i
-        const int u = rank * units + (i >> 2), col = 4 * (u >> 4) + (i & 3), f = t.f0 + 8 * (u & 15);
-        if (MODE != LIN_FWD || i >= 4 * my_units || col >= t.ncols || f >= p.F) return;
-        if (p.bias) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
-        if (p.residual) res0 = *reinterpret_cast<const uint4*>(p.residual + (split_row + col) * p.F + f);
+    auto load_residual = [&](int i) {
+        if (MODE == LIN_FWD && p.residual && i < 4 * my_units && split_col(i) < t.ncols && split_f < p.F)
+            res0 = *reinterpret_cast<const uint4*>(p.residual + (split_row + split_col(i)) * p.F + split_f);
     };
     if (!p.offsets) {
         if (MODE != LIN_DW && warp == 0 && t.e >= 0 && elect_one()) {
@@ -650,9 +646,10 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         for (bool ok = true; t.e >= 0 && ok; advance(true)) {
             const bool any = t.k0 < t.k1;
             const int64_t row0 = out_row(t);
-            if (SPLIT && sent) {
+            if (SPLIT) {
                 if (threadIdx.x == 128) mbar_arrive_expect_tx(&sm->sums_full, (p.split - 1) * my_units * 128);
-                load_ends(threadIdx.x - 128);   // under the sums: what the end of the tile reads besides them
+                if (MODE == LIN_FWD && p.bias && split_f < p.F) bias0 = *reinterpret_cast<const uint4*>(p.bias + split_f);
+                load_residual(i0);
                 bool got = any;
                 if (any) {
                     got = mbar_wait(&sm->acc_full[0], 0, &sm->status);
@@ -687,26 +684,6 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sm->sums_full);
                 break;     // a split tile is its cluster's only one
-            }
-            if (SPLIT) {   // partial sums [col][128], read by the others below
-                if (any) {
-                    if (!mbar_wait(&sm->acc_full[0], 0, &sm->status)) break;
-                    tc_fence_after();
-                }
-                for (int cc = (warp - 4) >> 2; cc * 32 < t.ncols; cc += 2) {
-                    uint32_t v[32];
-                    if (any) {
-                        tmem_ld32(tmem + (uint32_t(32 * ew) << 16) + cc * 32, v);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0u;
-                    }
-                    float* red = reinterpret_cast<float*>(base) + cc * 32 * 128 + ew * 32 + lane;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (cc * 32 + j < t.ncols) red[j * 128] = __uint_as_float(v[j]);
-                }
-                break;
             }
             for (int sub = 0; sub < subs(t); ++sub) {
                 const int ncols = sub_cols(t, sub);
@@ -748,55 +725,29 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             }
         }
     }
-    if (SPLIT && sent) {
+    if (SPLIT) {
         __syncwarp();
         if (p.split > 1) cluster_arrive();       // this CTA has sent what it sends
         bool ok = true;
         if (warp >= 4 && t.e >= 0) {
             ok = mbar_wait(&sm->sums_full, 0, &sm->status);
-            // a thread has eight features of one column
-            for (int i = threadIdx.x - 128; i < 4 * my_units; i += LN_EPI_THREADS) {
-                const int at = i >> 2, u = rank * units + at, col = 4 * (u >> 4) + (i & 3), f = t.f0 + 8 * (u & 15);
-                const uint4 bias = bias0, res = res0;
-                load_ends(i + LN_EPI_THREADS);   // of the next piece, under this one's sums
+            for (int i = i0; i < 4 * my_units; i += LN_EPI_THREADS) {
+                const uint4 res = res0;
+                load_residual(i + LN_EPI_THREADS);
+                const int at = i >> 2;
                 const float* q = reinterpret_cast<const float*>(sums_at) + at * 32 + (i & 3);
                 float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 for (int s = 0; s < p.split; ++s)
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[j] += q[s * units * 32 + ((j + at) & 7) * 4];
-                if (col < t.ncols && f < p.F) finish8<MODE>(p, (split_row + col) * p.F + f, v, bias, res);
+                if (split_col(i) < t.ncols && split_f < p.F)
+                    finish8<MODE>(p, (split_row + split_col(i)) * p.F + split_f, v, bias0, res);
             }
         }
         __syncwarp();
         if (p.split > 1) cluster_wait();
         // a wait that gave up: all has been sent, and lands before this CTA leaves
         if (!ok) mbar_wait(&sm->sums_full, 0, nullptr);
-    } else if (SPLIT) {
-        // every CTA's partial sums are in its shared memory
-        __syncwarp();
-        if (p.split > 1) cluster_sync();
-        else __syncthreads();
-        if (warp >= 4 && t.e >= 0) {
-            // 16 threads to a column, each with eight features
-            const int f8 = 8 * (threadIdx.x & 15), f = t.f0 + f8, step = p.split * (LN_EPI_THREADS / 16);
-            const float* red = reinterpret_cast<const float*>(base) + f8;
-            for (int col = rank * (LN_EPI_THREADS / 16) + (threadIdx.x - 128) / 16; col < t.ncols && f < p.F; col += step) {
-                const int64_t idx = (split_row + col) * p.F + f;
-                if (MODE == LIN_FWD && p.residual) res0 = *reinterpret_cast<const uint4*>(p.residual + idx);
-                if (MODE == LIN_FWD && p.bias) bias0 = *reinterpret_cast<const uint4*>(p.bias + f);
-                float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-                for (int s = 0; s < p.split; ++s) {
-                    const float4 a = ld_dsmem_f32x4(red + col * 128, s);
-                    const float4 b = ld_dsmem_f32x4(red + col * 128 + 4, s);
-                    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-                    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-                }
-                finish8<MODE>(p, idx, v, bias0, res0);
-            }
-        }
-        __syncwarp();
-        if (p.split > 1) cluster_sync();         // no CTA leaves while another reads its shared memory
     }
     if (PAIR) {
         __syncwarp();
@@ -957,7 +908,7 @@ moe_status prefer_smem(void (*kernel)(KArgs...)) {
 // Chunks of all rows for pairs: the fewest that take the least time, counted as
 // rounds of tiles over the pairs times the cycles of a step, which are those of
 // the MMAs (2 a column) or of the loads (128 rows of A and half of the columns,
-// 64 bytes a cycle), whichever are more.
+// 64 bytes a cycle), whichever are more, and at least 480 (a step's latencies).
 // A tile of more than 256 leaves the tensor cores idle for about 5000 cycles at
 // its end, until its first accumulator has been read.
 int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
@@ -966,24 +917,144 @@ int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
     int64_t best_time = INT64_MAX;
     for (int c = least; c <= most; ++c) {
         const int n = (int(ceil_div(rows, c)) + 31) & ~31;
-        const int64_t tile = int64_t(steps) * (2 * n > n + 256 ? 2 * n : n + 256) + (n > 256 ? 5000 : 0);
+        const int64_t tile = int64_t(steps) * (n > 256 ? 2 * n : n < 224 ? 480 : n + 256) + (n > 256 ? 5000 : 0);
         const int64_t time = ceil_div(int64_t(c) * n_fblocks, pairs) * tile;
         if (time < best_time) best = c, best_time = time;
     }
     return best;
 }
 
+// The clusters of `split` CTAs that the device holds at once: with one CTA to an
+// SM 36 clusters of 4 do not fit 148 SMs, because a cluster stays within a GPC.
+template <typename... KArgs>
+int max_clusters(void (*kernel)(KArgs...), int split, int smem) {
+    static std::mutex mu;
+    static std::map<std::tuple<int, const void*, int, int>, int> known;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    const auto key = std::make_tuple(dev, reinterpret_cast<const void*>(kernel), split, smem);
+    const auto it = known.find(key);
+    if (it != known.end()) return it->second;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(split));
+    cfg.blockDim = dim3(LN_THREADS);
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+        return 0;
+    return known[key] = n;
+}
+
+// Shared memory of a split tile's CTA: its ring and, with more than one CTA, the
+// sums that it is sent; half of an SM's for tiles of up to 64 columns.
+struct SplitSmem {
+    int stages, ring, total;
+    SplitSmem(int bn, int split) {
+        const int stage = LN_A_BYTES + bn * 128, sums = split > 1 ? split * ((4 * bn + split - 1) / split) * 128 : 0;
+        stages = ((bn <= 64 ? LN_HALF_RING_BYTES : LN_FULL_RING_BYTES) - sums) / stage;
+        if (stages > LN_MAX_STAGES) stages = LN_MAX_STAGES;
+        ring = stages * stage;
+        if (split == 1 && ring < bn * 512) ring = bn * 512;   // a tile's own sums reuse the ring
+        total = 1024 + ring + LN_STG_OFFSET + sums;
+    }
+};
+
+// How a call's tiles are shared out, by an estimate of the cycles it takes: the
+// rounds of tiles over the SMs, times the steps of a tile, times a step's loads
+// (64 bytes a cycle) or MMAs, whichever take longer, and at least 480; and then
+// the last tile's epilogue and what a kernel costs before and after.  The
+// constants were measured on 64 to 16384 features and contractions of 64 to 16384.
 template <int MODE>
-moe_status launch_mode(const CUtensorMap& ta, const CUtensorMap& tb, const LinParams& p, int share, int sums,
-                       int64_t tiles, int sms, cudaStream_t stream) {
+moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinParams p, int sms, cudaStream_t stream) {
+    constexpr bool DW = MODE == LIN_DW;
+    const int experts = p.E < p.rows ? p.E : p.rows;
+    const int per_expert = int(ceil_div(p.rows, p.E)), steps = int(ceil_div(DW ? per_expert : p.C, 64));
+    const int fb = int(ceil_div(p.F, 128)), fb2 = int(ceil_div(p.F, 256));
+    // chunks of all rows (LIN_DW: blocks of all columns), at most
+    auto units = [&](int bn) {
+        return DW ? int64_t(p.E) * ceil_div(N, bn) : p.offsets ? int64_t(p.rows) / bn + experts : ceil_div(p.rows, bn);
+    };
+    // columns that a tile may have: as many as there are, or as an expert has rows
+    // on average -- and not below 64 then, since many rows of one expert in narrow
+    // tiles would stream its weights through every SM again and again
+    const int cols = DW ? N : !p.offsets || p.rows <= 64 ? p.rows : per_expert > 64 ? per_expert : 64;
+
+    int share = LIN_ONE;
+    p.bn = DW || cols > 32 ? (cols <= 64 ? 64 : cols <= 128 ? 128 : 256) : cols <= 16 ? 16 : 32;
+    p.split = 1;
+    int64_t best = ceil_div(units(p.bn) * fb, sms) * steps * (p.bn < 112 ? 480 : 256 + 2 * p.bn) + 20 * p.bn + 4000;
+    if (cols > 128) {
+        p.chunks = DW || p.offsets ? 0 : pair_chunks(p.rows, fb2, steps, sms / 2);
+        const int64_t n = p.chunks ? p.chunks : units(256), width = p.chunks ? (ceil_div(p.rows, p.chunks) + 31) & ~31 : 256;
+        const int64_t time = ceil_div(n * fb2, sms / 2) * steps * (width > 256 ? 2 * width : width < 224 ? 480 : 256 + width) + 20 * width + 4500;
+        if (time < best) best = time, share = LIN_PAIR;
+    }
+    for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 128; bn += DW ? 64 : 16) {
+        const int64_t tiles = units(bn) * fb;
+        if (tiles <= sms) {
+            int s = int(sms / tiles);
+            if (s > 8) s = 8;
+            if (s > steps) s = steps;
+            // two CTAs to an SM leave room for the clusters' gaps
+            while (s > 1 && bn > 64 && max_clusters(linear_kernel<MODE, LIN_SPLIT>, s, SplitSmem(bn, s).total) < tiles) --s;
+            for (; s >= 1; s = s > 1 ? 1 : 0) {
+                const int64_t time = ceil_div(steps, s) * (bn < 112 ? 480 : 256 + 2 * bn) + 20 * bn + (s > 1 ? 4000 : 2500);
+                if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
+            }
+        }
+        if (bn >= cols) break;
+    }
+
+    int64_t n_units = units(p.bn);
+    int smem = LN_SMEM_BYTES, cluster = 1, stage = LN_A_BYTES + p.bn * 128;
+    if (share == LIN_PAIR) {
+        cluster = 2;
+        p.bn = 256;
+        n_units = units(256);
+        if (!DW && p.offsets) p.bn = 320;
+        if (!DW && !p.offsets) {
+            n_units = p.chunks;
+            if (ceil_div(p.rows, p.chunks) > 256) p.bn = 320;
+        }
+        stage = LN_A_BYTES + p.bn / 2 * 128;
+    } else {
+        p.chunks = int(ceil_div(p.rows, p.bn));
+    }
+    if (share == LIN_SPLIT) {
+        const SplitSmem sizes(p.bn, p.split);
+        cluster = p.split;
+        p.stages = sizes.stages;
+        p.ring_bytes = sizes.ring;
+        smem = sizes.total;
+        p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : 128;
+    } else {
+        p.stages = LN_RING_BYTES / stage < LN_MAX_STAGES ? LN_RING_BYTES / stage : LN_MAX_STAGES;
+        p.ring_bytes = p.stages * stage;
+        p.tmem_cols = 512;
+    }
+    p.n_fblocks = share == LIN_PAIR ? fb2 : fb;
+    p.box = DW ? 64 : share == LIN_PAIR ? 32 : share == LIN_SPLIT || p.bn < 64 ? p.bn : 64;
+
+    CUtensorMap ta, tb;
+    const bool ok = DW ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
+                       : make_map(&ta, a, K, N, p.E, MODE == LIN_FWD ? 128 : 64) &&
+                             make_map(&tb, b, p.C, p.rows, 0, p.box);
+    if (!ok) return MOE_ERR_CUDA;
     auto kernel = share == LIN_PAIR    ? linear_kernel<MODE, LIN_PAIR>
                   : share == LIN_SPLIT ? linear_kernel<MODE, LIN_SPLIT>
                                        : linear_kernel<MODE, LIN_ONE>;
     if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
-    const size_t smem = 1024 + p.ring_bytes + LN_STG_OFFSET + (share == LIN_SPLIT ? sums : LN_EPI_WARPS * LN_STG_BYTES);
-    const int64_t cluster = share == LIN_PAIR ? 2 : share == LIN_SPLIT ? p.split : 1;
+    const int64_t tiles = n_units * p.n_fblocks;
     const int64_t grid = share == LIN_SPLIT ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
-    return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, smem, unsigned(cluster), stream, ta, tb, p);
+    return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, size_t(smem), unsigned(cluster), stream, ta, tb, p);
 }
 
 }  // namespace
@@ -996,61 +1067,9 @@ moe_status launch_linear(int mode, const bf16* a, const bf16* b, int32_t N, int3
     p.F = mode == LIN_FWD ? N : K;
     p.C = mode == LIN_FWD ? K : N;
     p.NC = N;
-    // columns of a tile: as many as there are (LIN_DW: n), or as an expert has
-    // rows on average -- and not below 64 then, since many rows of one expert in
-    // narrow tiles would stream its weights through every SM again and again
-    int64_t cols = mode == LIN_DW ? N : p.rows;
-    if (mode != LIN_DW && p.offsets && cols > 64) cols = ceil_div(p.rows, p.E) > 64 ? ceil_div(p.rows, p.E) : 64;
-    // (up to 320 for pairs: see row_chunks)
-    p.bn = cols <= 16 && mode != LIN_DW ? 16 : cols <= 32 && mode != LIN_DW ? 32 : cols <= 64 ? 64 : cols <= 128 ? 128 : 256;
-    const int64_t units = mode == LIN_DW ? p.E * ceil_div(N, p.bn)
-                          : p.offsets    ? p.rows / p.bn + (p.E < p.rows ? p.E : p.rows)   // at most
-                                         : ceil_div(p.rows, p.bn);
-    const int64_t tiles = units * ceil_div(p.F, 128);
-    const int64_t steps = ceil_div(mode == LIN_DW ? ceil_div(p.rows, p.E) : p.C, 64);
-    // wide tiles go to pairs of CTAs, unless there are so few that more than
-    // half of the pairs had none; few tiles are split along the contraction
-    int share = LIN_ONE;
-    p.split = 1;
-    if (p.bn == 256 && 2 * units * ceil_div(p.F, 256) > sms / 2) {
-        share = LIN_PAIR;
-    } else if (p.bn <= 64 ? tiles <= sms : 2 * tiles <= sms) {
-        share = LIN_SPLIT;
-        int64_t s = sms / tiles;
-        if (s > 8) s = 8;
-        if (s > steps / 4) s = steps / 4;
-        if (s > 1) p.split = int(s);
-    }
-    p.n_fblocks = int(ceil_div(p.F, share == LIN_PAIR ? 256 : 128));
-    p.chunks = int(ceil_div(p.rows, p.bn));
-    int64_t n_units = units;
-    if (share == LIN_PAIR && mode != LIN_DW) {
-        if (p.offsets) {
-            p.bn = 320;
-        } else {
-            p.chunks = pair_chunks(p.rows, p.n_fblocks, int(steps), sms / 2);
-            n_units = p.chunks;
-            if (ceil_div(p.rows, p.chunks) > 256) p.bn = 320;
-        }
-    }
-    p.box = mode == LIN_DW ? 64 : share == LIN_PAIR ? 32 : p.bn < 64 ? p.bn : 64;
-    const int stage = LN_A_BYTES + (share == LIN_PAIR ? p.bn / 2 : p.bn) * 128;
-    const bool half = share == LIN_SPLIT && p.bn <= 64;
-    const int sums = half && p.split > 1 ? p.split * int(ceil_div(4 * p.bn, p.split)) * 128 : 0;
-    p.stages = (half ? LN_HALF_RING_BYTES - sums : LN_RING_BYTES) / stage;
-    if (p.stages > LN_MAX_STAGES) p.stages = LN_MAX_STAGES;
-    p.ring_bytes = p.stages * stage;
-    // the partial sums of a tile that is not split, or is wide, reuse the ring
-    if (share == LIN_SPLIT && !sums && p.ring_bytes < p.bn * 512) p.ring_bytes = p.bn * 512;
-    p.tmem_cols = share == LIN_SPLIT ? (p.bn < 32 ? 32 : p.bn) : 512;
-    CUtensorMap ta, tb;
-    const bool ok = mode == LIN_DW
-        ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
-        : make_map(&ta, a, K, N, p.E, mode == LIN_FWD ? 128 : 64) && make_map(&tb, b, p.C, p.rows, 0, p.box);
-    if (!ok) return MOE_ERR_CUDA;
-    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
-    if (mode == LIN_DX) return launch_mode<LIN_DX>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
-    return launch_mode<LIN_DW>(ta, tb, p, share, sums, n_units * p.n_fblocks, sms, stream);
+    if (mode == LIN_FWD) return launch_mode<LIN_FWD>(a, b, N, K, p, sms, stream);
+    if (mode == LIN_DX) return launch_mode<LIN_DX>(a, b, N, K, p, sms, stream);
+    return launch_mode<LIN_DW>(a, b, N, K, p, sms, stream);
 }
 
 moe_status launch_act_grad(const bf16* dy, const bf16* z, int32_t T, int32_t N, int32_t act, bf16* dz, void* dbias,
