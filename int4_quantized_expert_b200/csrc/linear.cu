@@ -38,8 +38,8 @@
 // scan over the (at most 256) experts.
 //
 // LIN_SPLIT: when the tiles fit the SMs at once, a CTA takes one tile of up to
-// 128 columns, or a cluster of up to 8 CTAs shares one tile's contraction and each
-// finishes a part of the tile.  Partial sums are sent to the CTA that finishes
+// 128 columns, or a cluster of up to 8 CTAs shares the contraction of one of up to
+// 192 and each finishes a part of the tile.  Partial sums are sent to the CTA that finishes
 // them (st.async to its shared memory, counted by a barrier there) and added in
 // rank order: no scratch, no atomics, the same bits every time.  Short calls are
 // bound by latency or by the weights' bytes, so what counts is how soon a call's
@@ -735,11 +735,12 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 const uint4 res = res0;
                 load_residual(i + LN_EPI_THREADS);
                 const int at = i >> 2;
-                const float* q = reinterpret_cast<const float*>(sums_at) + at * 32 + (i & 3);
+                uint32_t q = smem_u32(sums_at) + at * 128 + (i & 3) * 4;
                 float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-                for (int s = 0; s < p.split; ++s)
+#pragma unroll 4
+                for (int s = 0; s < p.split; ++s, q += units * 128)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += q[s * units * 32 + ((j + at) & 7) * 4];
+                    for (int j = 0; j < 8; ++j) v[j] += ld_shared_f32_at(q + ((j + at) & 7) * 16);
                 if (split_col(i) < t.ncols && split_f < p.F)
                     finish8<MODE>(p, (split_row + split_col(i)) * p.F + split_f, v, bias0, res);
             }
@@ -997,7 +998,7 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         const int64_t time = ceil_div(n * fb2, sms / 2) * steps * (width > 256 ? 2 * width : width < 224 ? 480 : 256 + width) + 20 * width + 4500;
         if (time < best) best = time, share = LIN_PAIR;
     }
-    for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 128; bn += DW ? 64 : 16) {
+    for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 192; bn += DW ? 64 : 16) {
         const int64_t tiles = units(bn) * fb;
         if (tiles <= sms) {
             int s = int(sms / tiles);
@@ -1005,7 +1006,8 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
             if (s > steps) s = steps;
             // two CTAs to an SM leave room for the clusters' gaps
             while (s > 1 && bn > 64 && max_clusters(linear_kernel<MODE, LIN_SPLIT>, s, SplitSmem(bn, s).total) < tiles) --s;
-            for (; s >= 1; s = s > 1 ? 1 : 0) {
+            // wider than 128, a tile that is not split is a whole pair's or another kernel's
+            for (; s >= 1 && (s > 1 || bn <= 128); s = s > 1 ? 1 : 0) {
                 const int64_t time = ceil_div(steps, s) * (bn < 112 ? 480 : 256 + 2 * bn) + 20 * bn + (s > 1 ? 4000 : 2500);
                 if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
             }
@@ -1034,7 +1036,7 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         p.stages = sizes.stages;
         p.ring_bytes = sizes.ring;
         smem = sizes.total;
-        p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : 128;
+        p.tmem_cols = p.bn <= 32 ? 32 : p.bn <= 64 ? 64 : p.bn <= 128 ? 128 : 256;
     } else {
         p.stages = LN_RING_BYTES / stage < LN_MAX_STAGES ? LN_RING_BYTES / stage : LN_MAX_STAGES;
         p.ring_bytes = p.stages * stage;
