@@ -62,9 +62,8 @@
 // step of loads and MMAs took 710; this way it takes 530.
 #include <cuda.h>
 
+#include <atomic>
 #include <cstdint>
-#include <map>
-#include <tuple>
 #include <type_traits>
 
 #include "activation.cuh"
@@ -925,35 +924,6 @@ int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
     return best;
 }
 
-// The clusters of `split` CTAs that the device holds at once: with one CTA to an
-// SM 36 clusters of 4 do not fit 148 SMs, because a cluster stays within a GPC.
-template <typename... KArgs>
-int max_clusters(void (*kernel)(KArgs...), int split, int smem) {
-    static std::mutex mu;
-    static std::map<std::tuple<int, const void*, int, int>, int> known;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(dev, reinterpret_cast<const void*>(kernel), split, smem);
-    const auto it = known.find(key);
-    if (it != known.end()) return it->second;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(split));
-    cfg.blockDim = dim3(LN_THREADS);
-    cfg.dynamicSmemBytes = size_t(smem);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = unsigned(split);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK ||
-        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
-        return 0;
-    return known[key] = n;
-}
-
 // Shared memory of a split tile's CTA: its ring and, with more than one CTA, the
 // sums that it is sent; half of an SM's for tiles of up to 64 columns.
 struct SplitSmem {
@@ -968,11 +938,40 @@ struct SplitSmem {
     }
 };
 
+// The clusters of `split` CTAs that a device holds at once, one CTA to an SM: 33 of
+// 4 on 148 SMs, because a cluster stays within a GPC.  0 if it cannot be found out.
+int max_clusters(int split) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][9];   // + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+    const int have = known[dev][split].load(std::memory_order_relaxed);
+    if (have) return have - 1;
+    auto kernel = linear_kernel<LIN_FWD, LIN_SPLIT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(split));
+    cfg.blockDim = dim3(LN_THREADS);
+    cfg.dynamicSmemBytes = size_t(SplitSmem(128, split).total);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(split);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (allow_max_smem(kernel) != MOE_OK || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+    known[dev][split].store(n + 1, std::memory_order_relaxed);
+    return n;
+}
+
 // How a call's tiles are shared out, by an estimate of the cycles it takes: the
 // rounds of tiles over the SMs, times the steps of a tile, times a step's loads
-// (64 bytes a cycle) or MMAs, whichever take longer, and at least 480; and then
-// the last tile's epilogue and what a kernel costs before and after.  The
-// constants were measured on 64 to 16384 features and contractions of 64 to 16384.
+// (64 bytes a cycle for an SM) or MMAs, whichever take longer, and at least 480;
+// the time that the weights take from HBM at 3400 bytes a cycle, an eighth more
+// where no SM has two CTAs (one to an SM, they end 10 % apart: 16 x 5120 -> 16384
+// takes 32.2 us in 128 CTAs and 28.9 in 256); and then the last tile's epilogue
+// and what a kernel costs before and after.  The constants were measured on 64 to
+// 16384 features and contractions of 64 to 16384.
 template <int MODE>
 moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinParams p, int sms, cudaStream_t stream) {
     constexpr bool DW = MODE == LIN_DW;
@@ -991,26 +990,35 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
     int share = LIN_ONE;
     p.bn = DW || cols > 32 ? (cols <= 64 ? 64 : cols <= 128 ? 128 : 256) : cols <= 16 ? 16 : 32;
     p.split = 1;
-    int64_t best = ceil_div(units(p.bn) * fb, sms) * steps * (p.bn < 112 ? 480 : 256 + 2 * p.bn) + 20 * p.bn + 4000;
+    const int64_t hbm = DW ? 0 : int64_t(p.offsets ? experts : 1) * N * K * 2 / 3400;
+    auto loop = [&](int64_t cycles, bool shared_sms) {
+        const int64_t least = shared_sms ? hbm : hbm + hbm / 8;
+        return cycles > least ? cycles : least;
+    };
+    int64_t best = loop(ceil_div(units(p.bn) * fb, sms) * steps * (p.bn < 112 ? 480 : 256 + 2 * p.bn), false) +
+                   20 * p.bn + 4000;
     if (cols > 128) {
         p.chunks = DW || p.offsets ? 0 : pair_chunks(p.rows, fb2, steps, sms / 2);
         const int64_t n = p.chunks ? p.chunks : units(256), width = p.chunks ? (ceil_div(p.rows, p.chunks) + 31) & ~31 : 256;
-        const int64_t time = ceil_div(n * fb2, sms / 2) * steps * (width > 256 ? 2 * width : width < 224 ? 480 : 256 + width) + 20 * width + 4500;
+        const int64_t step = width > 256 ? 2 * width : width < 224 ? 480 : 256 + width;
+        const int64_t time = loop(ceil_div(n * fb2, sms / 2) * steps * step, false) + 20 * width + 4500;
         if (time < best) best = time, share = LIN_PAIR;
     }
     for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 192; bn += DW ? 64 : 16) {
         const int64_t tiles = units(bn) * fb;
-        if (tiles <= sms) {
-            int s = int(sms / tiles);
+        // as many CTAs to a tile as two to an SM or one to an SM allow, or one;
+        // wider than 128, a tile that is not split is a pair's or another kernel's
+        for (int per_sm = bn <= 64 ? 2 : 1; tiles <= sms && per_sm >= 0; --per_sm) {
+            int s = per_sm ? int(per_sm * sms / tiles) : 1;
             if (s > 8) s = 8;
             if (s > steps) s = steps;
-            // two CTAs to an SM leave room for the clusters' gaps
-            while (s > 1 && bn > 64 && max_clusters(linear_kernel<MODE, LIN_SPLIT>, s, SplitSmem(bn, s).total) < tiles) --s;
-            // wider than 128, a tile that is not split is a whole pair's or another kernel's
-            for (; s >= 1 && (s > 1 || bn <= 128); s = s > 1 ? 1 : 0) {
-                const int64_t time = ceil_div(steps, s) * (bn < 112 ? 480 : 256 + 2 * bn) + 20 * bn + (s > 1 ? 4000 : 2500);
-                if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
-            }
+            while (s > 1 && (bn <= 64 ? 2 : 1) * max_clusters(s) < tiles) --s;
+            if (s == 1 && bn > 128) continue;
+            const bool shared_sms = s * tiles > sms;
+            const int load = (shared_sms ? 2 : 1) * (256 + 2 * bn);
+            const int64_t time = loop(ceil_div(steps, s) * (load < 480 ? 480 : load), shared_sms) + 20 * bn +
+                                 (s > 1 ? 5000 + 150 * s : 2500);
+            if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
         }
         if (bn >= cols) break;
     }
