@@ -84,6 +84,21 @@ def test_linear_forward_few_rows_and_long_sums(T, K, N):
     forward_case(T, K, N, "none", True, True, False, seed=11)
 
 
+# tiles of 16 to 192 rows whose contraction is split over up to 8 CTAs: rows
+# around the tiles' ends, features around a block's, contractions that leave some
+# CTAs a step more than others
+@pytest.mark.parametrize("T", [1, 3, 4, 5, 17, 33, 47, 63, 79, 96, 111, 128, 130, 144, 159, 176, 191, 192, 193])
+def test_linear_split_tiles(T):
+    forward_case(T, 1096, 264, "gelu", True, True, True, seed=T)
+    forward_case(T, 4104, 72, "none", False, True, False, seed=T + 1)
+
+
+@pytest.mark.parametrize("T,K,N", [(100, 40, 3000), (192, 264, 1608), (3, 136, 5128), (1100, 72, 200), (2000, 8, 8)])
+def test_linear_backward_split_tiles(T, K, N):
+    backward_case(T, K, N, "silu", torch.bfloat16, seed=17)
+    backward_case(T, N, K, "gelu", torch.float32, seed=18)
+
+
 # tiles of 256 features shared by two CTAs: rows around their chunks' ends (32,
 # 192, 256 and 320 rows, two accumulators from 257 on), features around 256,
 # contractions around 16 and 64

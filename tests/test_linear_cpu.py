@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import int4_quantized_expert_b200 as moe
+from tests import test_build_resources as resources
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 S = moe.Status
@@ -121,3 +122,9 @@ class _FakeCuda:
 
     def dim(self):
         return self._t.dim()
+
+
+@pytest.mark.parametrize("src,kernels", [("linear.cu", ["linear_kernel", "act_grad_kernel"]), ("swiglu.cu", ["swiglu_kernel"])])
+def test_kernels_do_not_spill(src, kernels, tmp_path, monkeypatch):
+    monkeypatch.setitem(resources.HOT, src, kernels)
+    resources.test_hot_kernels_do_not_spill(src, tmp_path)
