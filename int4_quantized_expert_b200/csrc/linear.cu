@@ -964,14 +964,16 @@ int max_clusters(int split) {
     return n;
 }
 
-// How a call's tiles are shared out, by an estimate of the cycles it takes: the
-// rounds of tiles over the SMs, times the steps of a tile, times a step's loads
-// (64 bytes a cycle for an SM) or MMAs, whichever take longer, and at least 480;
-// the time that the weights take from HBM at 3400 bytes a cycle, an eighth more
-// where no SM has two CTAs (one to an SM, they end 10 % apart: 16 x 5120 -> 16384
-// takes 32.2 us in 128 CTAs and 28.9 in 256); and then the last tile's epilogue
-// and what a kernel costs before and after.  The constants were measured on 64 to
-// 16384 features and contractions of 64 to 16384.
+// How a call's tiles are shared out, by an estimate of the cycles it takes.  A tile's
+// steps take their loads (64 bytes a cycle for an SM) or MMAs, whichever take
+// longer, and at least 480 each; its epilogue takes 20 cycles a column and more
+// with activation, residual or pre-activations, and 50 more through the sums of
+// LIN_SPLIT, over its CTAs.  Rounds of tiles over the SMs take
+// the longer of the two, all loops at least what the weights take from HBM at 3400
+// bytes a cycle (an eighth more where no SM has two CTAs: one to an SM, they end
+// 10 % apart; 16 x 5120 -> 16384 takes 32.2 us in 128 CTAs and 28.9 in 256); then
+// come the last epilogue and what a kernel costs before and after.  The constants
+// were measured on 64 to 16384 features and contractions of 64 to 16384.
 template <int MODE>
 moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinParams p, int sms, cudaStream_t stream) {
     constexpr bool DW = MODE == LIN_DW;
@@ -995,13 +997,17 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         const int64_t least = shared_sms ? hbm : hbm + hbm / 8;
         return cycles > least ? cycles : least;
     };
-    int64_t best = loop(ceil_div(units(p.bn) * fb, sms) * steps * (p.bn < 112 ? 480 : 256 + 2 * p.bn), false) +
-                   20 * p.bn + 4000;
+    const int column = 20 + (p.preact ? 10 : 0) + (p.residual ? 10 : 0) + (p.act == MOE_ACT_GELU ? 16 : p.act ? 8 : 0);
+    auto rounds = [&](int64_t n, int64_t tile_loop, int64_t epilogue) {
+        return loop(n * (tile_loop > epilogue ? tile_loop : epilogue), false) + epilogue;
+    };
+    int64_t best = rounds(ceil_div(units(p.bn) * fb, sms), steps * int64_t(p.bn < 112 ? 480 : 256 + 2 * p.bn),
+                          column * p.bn) + 4000;
     if (cols > 128) {
         p.chunks = DW || p.offsets ? 0 : pair_chunks(p.rows, fb2, steps, sms / 2);
         const int64_t n = p.chunks ? p.chunks : units(256), width = p.chunks ? (ceil_div(p.rows, p.chunks) + 31) & ~31 : 256;
         const int64_t step = width > 256 ? 2 * width : width < 224 ? 480 : 256 + width;
-        const int64_t time = loop(ceil_div(n * fb2, sms / 2) * steps * step, false) + 20 * width + 4500;
+        const int64_t time = rounds(ceil_div(n * fb2, sms / 2), steps * step, column * width) + 4500;
         if (time < best) best = time, share = LIN_PAIR;
     }
     for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 192; bn += DW ? 64 : 16) {
@@ -1016,9 +1022,16 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
             if (s == 1 && bn > 128) continue;
             const bool shared_sms = s * tiles > sms;
             const int load = (shared_sms ? 2 : 1) * (256 + 2 * bn);
-            const int64_t time = loop(ceil_div(steps, s) * (load < 480 ? 480 : load), shared_sms) + 20 * bn +
-                                 (s > 1 ? 5000 + 150 * s : 2500);
+            const int64_t time = loop(ceil_div(steps, s) * (load < 480 ? 480 : load), shared_sms) +
+                                 (column + 50 / s) * bn + (s > 1 ? 5000 + 150 * s : 2500);
             if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
+        }
+        // more tiles than SMs, two CTAs to an SM: one's epilogue under the other's loads
+        if (bn <= 64 && tiles > sms && tiles <= 8 * sms) {
+            const int load = 2 * (256 + 2 * bn);
+            const int64_t time = loop(ceil_div(tiles, 2 * sms) * (int64_t(steps) * (load < 480 ? 480 : load) + (column + 50) * bn + 2500),
+                                      true) + 2500;
+            if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = 1;
         }
         if (bn >= cols) break;
     }
