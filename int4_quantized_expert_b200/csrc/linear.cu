@@ -37,6 +37,10 @@
 // cycle that an SM can load are what bounds narrow tiles.  Each CTA derives the list from the offsets by a
 // scan over the (at most 256) experts.
 //
+// LIN_PAIR_SPLIT: where there are few such tiles, two to four pairs of a cluster
+// share one's contraction, as in LIN_SPLIT below; their rings take the sums once all
+// are past their MMAs.
+//
 // LIN_SPLIT: when the tiles fit the SMs at once, a CTA takes one tile of up to
 // 128 columns, or a cluster of up to 8 CTAs shares the contraction of one of up to
 // 192 and each finishes a part of the tile.  Partial sums are sent to the CTA that finishes
@@ -87,9 +91,11 @@ constexpr int LN_STG_BYTES = 32 * 64;     // an epilogue warp's staging buffer: 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
 static __device__ int32_t g_linear_status;
 
-// How CTAs share tiles: one tile each, a cluster per tile along the
-// contraction, or two CTAs per tile of 256 features.
-enum LinShare { LIN_ONE, LIN_SPLIT, LIN_PAIR };
+// How CTAs share tiles: one tile each, a cluster per tile along the contraction,
+// two CTAs per tile of 256 features, or a cluster of pairs per such tile.
+enum LinShare { LIN_ONE, LIN_SPLIT, LIN_PAIR, LIN_PAIR_SPLIT };
+__host__ __device__ constexpr bool is_pair(int share) { return share == LIN_PAIR || share == LIN_PAIR_SPLIT; }
+__host__ __device__ constexpr bool is_split(int share) { return share == LIN_SPLIT || share == LIN_PAIR_SPLIT; }
 
 struct alignas(16) Tile {
     int e, f0;            // expert (-1: there is no tile), the CTA's first feature
@@ -155,7 +161,7 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
     // an expert feature blocks in groups of 2048 features, chunk by chunk within a
     // group: the concurrent tiles of 148 CTAs then share 2048 features and 9 row
     // chunks.
-    constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
+    constexpr bool PAIR = is_pair(SHARE), SPLIT = is_split(SHARE);
     Tile t;
     int n, before;                         // the expert's chunks (LIN_DW: column blocks), those before it
     const int unit = tile / p.n_fblocks;   // not the tile's chunk, but one of its expert's
@@ -176,7 +182,7 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
     const int gf = min(PAIR ? 8 : 16, p.n_fblocks);
     const int in_e = tile - before * p.n_fblocks, g = in_e / (n * gf), r = in_e - g * n * gf;
     const int gsize = min(gf, p.n_fblocks - g * gf), i = r / gsize, fb = g * gf + (r - i * gsize);
-    t.f0 = 128 * (PAIR ? 2 * fb + rank : fb);
+    t.f0 = 128 * (PAIR ? 2 * fb + (rank & 1) : fb);
     if (MODE == LIN_DW) {
         t.col0 = i * p.bn;
         t.ncols = min(p.bn, p.NC - t.col0);
@@ -192,8 +198,9 @@ __device__ __forceinline__ Tile get_tile(int tile, const LinSmem* sm, const LinP
         t.clen = p.C;
     }
     const int nk = (t.clen + 63) >> 6;
-    t.k0 = SPLIT ? nk * rank / p.split : 0;
-    t.k1 = SPLIT ? nk * (rank + 1) / p.split : nk;
+    const int part = PAIR ? rank >> 1 : rank;
+    t.k0 = SPLIT ? nk * part / p.split : 0;
+    t.k1 = SPLIT ? nk * (part + 1) / p.split : nk;
     return t;
 }
 
@@ -339,12 +346,15 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     LinSmem* sm = reinterpret_cast<LinSmem*>(base + p.ring_bytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr bool A_MN = MODE != LIN_FWD, B_MN = MODE == LIN_DW;
-    constexpr bool PAIR = SHARE == LIN_PAIR, SPLIT = SHARE == LIN_SPLIT;
+    constexpr bool PAIR = is_pair(SHARE), SPLIT = is_split(SHARE);
     constexpr bool HAND_OVER = PAIR || MODE == LIN_DW;
     const int stage_bytes = LN_A_BYTES + (PAIR ? p.bn / 2 : p.bn) * 128;
     uint32_t rank = 0;
     if (SHARE != LIN_ONE) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    const bool leader = !PAIR || rank == 0;   // issues the MMAs
+    // of a pair: the CTA's half of the features, the rank of the one that issues the
+    // MMAs, both as a mask; the CTA's (pair's) part of a split contraction
+    const uint32_t half = PAIR ? rank & 1 : 0, lead = rank & ~1u, both_ctas = 3u << lead, part = PAIR ? rank >> 1 : rank;
+    const bool leader = half == 0;
 
     griddep_launch_dependents();
     if (warp == 0) {
@@ -417,11 +427,11 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     const uint32_t tmem = sm->tmem_base;
     const int n_units = MODE == LIN_DW ? p.E * ((p.NC + p.bn - 1) / p.bn) : sm->first[p.E];
     const int n_tiles = n_units * p.n_fblocks;
-    const int tile0 = SPLIT ? int(blockIdx.x) / p.split : PAIR ? int(blockIdx.x) / 2 : int(blockIdx.x);
+    const int tile0 = int(blockIdx.x) / ((PAIR ? 2 : 1) * (SPLIT ? p.split : 1));
     const int tstep = PAIR ? int(gridDim.x) / 2 : int(gridDim.x);
     // the accumulators of a tile: MMA's N, and the rows of B (the columns of D)
     // that this CTA loads
-    constexpr bool WIDE = PAIR && MODE != LIN_DW;
+    constexpr bool WIDE = SHARE == LIN_PAIR && MODE != LIN_DW;
     auto subs = [](const Tile& t) { return WIDE && t.ncols > 256 ? 2 : 1; };
     auto sub_cols = [&](const Tile& t, int i) { return subs(t) == 1 ? t.ncols : i == 0 ? LN_SUB : t.ncols - LN_SUB; };
     auto mma_n = [](int ncols) { return PAIR ? (ncols + 31) & ~31 : (ncols + 15) & ~15; };
@@ -453,14 +463,14 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     // the eight units a warp reads at a time have in different banks.
     const int64_t split_row = SPLIT ? out_row(t) : 0;
     const int n_sums = (t.ncols + 3) / 4 * 16, units = (n_sums + p.split - 1) / p.split;
-    const int my_units = max(0, min(units, n_sums - int(rank) * units));
-    unsigned char* sums_at = p.split > 1 ? reinterpret_cast<unsigned char*>(sm) + LN_STG_OFFSET : base;
+    const int my_units = max(0, min(units, n_sums - int(part) * units));
+    unsigned char* sums_at = !PAIR && p.split > 1 ? reinterpret_cast<unsigned char*>(sm) + LN_STG_OFFSET : base;
     // A thread finishes eight features of a column at a time, LN_EPI_THREADS / 4
     // units apart: its features stay the same.  The bias and the first residual are
     // loaded under the sums, each next residual under the piece before.
     const int i0 = int(threadIdx.x) - 128;
-    const int split_f = t.f0 + 8 * ((int(rank) * units + (i0 >> 2)) & 15);
-    auto split_col = [&](int i) { return 4 * ((int(rank) * units + (i >> 2)) >> 4) + (i & 3); };
+    const int split_f = t.f0 + 8 * ((int(part) * units + (i0 >> 2)) & 15);
+    auto split_col = [&](int i) { return 4 * ((int(part) * units + (i >> 2)) >> 4) + (i & 3); };
     uint4 bias0 = make_uint4(0, 0, 0, 0), res0 = bias0;
     auto load_residual = [&](int i) {
         if (MODE == LIN_FWD && p.residual && i < 4 * my_units && split_col(i) < t.ncols && split_f < p.F)
@@ -489,8 +499,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             for (; t.e >= 0 && ok; advance(false)) {
                 const int n0 = sub_cols(t, 0), n1 = subs(t) > 1 ? t.ncols - n0 : 0;
                 const int boxes0 = b_boxes(n0), boxes = boxes0 + (WIDE ? b_boxes(n1) : 0);
-                const int row = t.col0 + (PAIR ? int(rank) * b_rows(n0) : 0);
-                const int row1 = t.col0 + n0 + int(rank) * b_rows(n1) - boxes0 * p.box;   // so box i is at row1 + i * p.box
+                const int row = t.col0 + int(half) * b_rows(n0);
+                const int row1 = t.col0 + n0 + int(half) * b_rows(n1) - boxes0 * p.box;   // so box i is at row1 + i * p.box
                 const int box_bytes = p.box * 128;
                 const uint32_t bytes = LN_A_BYTES + boxes * box_bytes;
                 for (int kk = t.k0; kk < t.k1; ++kk) {
@@ -568,7 +578,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                             else umma<false>(d0, a, b, idesc0, accumulate);
                             if (decltype(two)::value) umma_pair(d1, a, b + (LN_SUB / 2 * 128 >> 4), idesc1, accumulate);
                         }
-                    if (PAIR) umma_commit_pair(&sm->empty[slot]);
+                    if (PAIR) umma_commit_pair(&sm->empty[slot], both_ctas);
                     else umma_commit(&sm->empty[slot]);
                     if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
                 }
@@ -584,12 +594,12 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 if (WIDE && n1) ok = steps(std::true_type{}, d0, idesc0, d1, idesc1);
                 else ok = steps(std::false_type{}, d0, idesc0, 0, 0);
                 if (!ok) break;
-                if (WIDE && n1) umma_commit_pair(&sm->acc_full[(n - 2) % LN_ACCS]);
-                if (PAIR) umma_commit_pair(&sm->acc_full[(n - 1) % LN_ACCS]);
+                if (WIDE && n1) umma_commit_pair(&sm->acc_full[(n - 2) % LN_ACCS], both_ctas);
+                if (PAIR) umma_commit_pair(&sm->acc_full[(n - 1) % LN_ACCS], both_ctas);
                 else umma_commit(&sm->acc_full[(n - 1) % LN_ACCS]);
             }
             // wind down: wait (bounded) for the last MMAs
-            if (PAIR) umma_commit_pair(&sm->drained);
+            if (PAIR) umma_commit_pair(&sm->drained, both_ctas);
             else umma_commit(&sm->drained);
             mbar_wait(&sm->drained, 0, nullptr);
         }
@@ -616,8 +626,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                 }
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR && ragged) mbar_arrive_at<true>(&sm->ready[slot], 0);
-                    else if (PAIR) mbar_arrive_at(&sm->ready[slot], 0);
+                    if (PAIR && ragged) mbar_arrive_at<true>(&sm->ready[slot], lead);
+                    else if (PAIR) mbar_arrive_at(&sm->ready[slot], lead);
                     else mbar_arrive(&sm->ready[slot]);
                 }
                 if (++slot == uint32_t(p.stages)) { slot = 0; par ^= 1; }
@@ -654,6 +664,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     got = mbar_wait(&sm->acc_full[0], 0, &sm->status);
                     tc_fence_after();
                 }
+                // pairs' sums reuse the rings: every pair is past its loads and MMAs
+                if (PAIR) { __syncwarp(); cluster_sync(); }
                 // 16-byte pieces of one feature and four columns, also after a
                 // wait that gave up: the others count on them
                 const uint32_t sums = smem_u32(sums_at);
@@ -670,11 +682,11 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
 #pragma unroll
                     for (int g = 0; g < 8; ++g) {
                         if (cc * 32 + 4 * g < t.ncols) {
-                            const uint32_t to = sums + ((rank * units + at) * 8 + ((lane + at) & 7)) * 16;
-                            if (owner == int(rank))
+                            const uint32_t to = sums + ((part * units + at) * 8 + ((lane + at) & 7)) * 16;
+                            if (owner == int(part))
                                 st_shared_v4_at(to, make_uint4(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]));
                             else
-                                st_async_v4(to, owner, &sm->sums_full, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+                                st_async_v4(to, PAIR ? 2 * owner + half : owner, &sm->sums_full, v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
                         }
                         at += 16;
                         while (at >= units) { at -= units; ++owner; }
@@ -698,7 +710,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
                     tc_fence_before();
                     __syncwarp();
                     if (any && lane == 0) {
-                        if (PAIR) mbar_arrive_at(&sm->acc_empty[n % LN_ACCS], 0);
+                        if (PAIR) mbar_arrive_at(&sm->acc_empty[n % LN_ACCS], lead);
                         else mbar_arrive(&sm->acc_empty[n % LN_ACCS]);
                     }
                 };
@@ -724,12 +736,13 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             }
         }
     }
+    bool landed = true;
     if (SPLIT) {
         __syncwarp();
-        if (p.split > 1) cluster_arrive();       // this CTA has sent what it sends
-        bool ok = true;
+        if (PAIR && (warp < 4 || t.e < 0)) cluster_sync();
+        if (!PAIR && p.split > 1) cluster_arrive();   // this CTA has sent what it sends
         if (warp >= 4 && t.e >= 0) {
-            ok = mbar_wait(&sm->sums_full, 0, &sm->status);
+            landed = mbar_wait(&sm->sums_full, 0, &sm->status);
             for (int i = i0; i < 4 * my_units; i += LN_EPI_THREADS) {
                 const uint4 res = res0;
                 load_residual(i + LN_EPI_THREADS);
@@ -745,9 +758,7 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
             }
         }
         __syncwarp();
-        if (p.split > 1) cluster_wait();
-        // a wait that gave up: all has been sent, and lands before this CTA leaves
-        if (!ok) mbar_wait(&sm->sums_full, 0, nullptr);
+        if (!PAIR && p.split > 1) cluster_wait();
     }
     if (PAIR) {
         __syncwarp();
@@ -755,6 +766,8 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         // ... and the last commit, which arrives in both CTAs, has arrived here
         if (threadIdx.x == 32) mbar_wait(&sm->drained, 0, nullptr);
     }
+    // a wait that gave up: all has been sent, and lands before this CTA leaves
+    if (SPLIT && !landed) mbar_wait(&sm->sums_full, 0, nullptr);
     tc_fence_before();
     __syncthreads();
     if (warp == 3) {
@@ -989,7 +1002,7 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
     // tiles would stream its weights through every SM again and again
     const int cols = DW ? N : !p.offsets || p.rows <= 64 ? p.rows : per_expert > 64 ? per_expert : 64;
 
-    int share = LIN_ONE;
+    int share = LIN_ONE, pair_split_chunks = 0;
     p.bn = DW || cols > 32 ? (cols <= 64 ? 64 : cols <= 128 ? 128 : 256) : cols <= 16 ? 16 : 32;
     p.split = 1;
     const int64_t hbm = DW ? 0 : int64_t(p.offsets ? experts : 1) * N * K * 2 / 3400;
@@ -1009,6 +1022,19 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         const int64_t step = width > 256 ? 2 * width : width < 224 ? 480 : 256 + width;
         const int64_t time = rounds(ceil_div(n * fb2, sms / 2), steps * step, column * width) + 4500;
         if (time < best) best = time, share = LIN_PAIR;
+    }
+    if (cols > 128 && !p.offsets) {
+        const int least = int(ceil_div(DW ? N : p.rows, 256));
+        for (int c = least; c <= (DW ? least : least + 2); ++c) {
+            const int width = DW ? 256 : int(ceil_div(p.rows, c) + 31) & ~31;
+            if (!DW && (c - 1) * width >= p.rows) continue;   // no chunk may be empty
+            for (int q = 2; q <= 4 && q <= steps; ++q) {
+                if (max_clusters(2 * q) < c * fb2) break;
+                const int64_t time = loop(ceil_div(steps, q) * (width < 224 ? 480 : 256 + width), false) +
+                                     (column + 50 / q) * width + 6000 + 300 * q;
+                if (time < best) best = time, share = LIN_PAIR_SPLIT, p.split = q, pair_split_chunks = c;
+            }
+        }
     }
     for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 192; bn += DW ? 64 : 16) {
         const int64_t tiles = units(bn) * fb;
@@ -1038,7 +1064,13 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
 
     int64_t n_units = units(p.bn);
     int smem = LN_SMEM_BYTES, cluster = 1, stage = LN_A_BYTES + p.bn * 128;
-    if (share == LIN_PAIR) {
+    if (share == LIN_PAIR_SPLIT) {
+        cluster = 2 * p.split;
+        p.bn = 256;
+        p.chunks = pair_split_chunks;
+        n_units = p.chunks;
+        stage = LN_A_BYTES + p.bn / 2 * 128;
+    } else if (share == LIN_PAIR) {
         cluster = 2;
         p.bn = 256;
         n_units = units(256);
@@ -1063,20 +1095,21 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         p.ring_bytes = p.stages * stage;
         p.tmem_cols = 512;
     }
-    p.n_fblocks = share == LIN_PAIR ? fb2 : fb;
-    p.box = DW ? 64 : share == LIN_PAIR ? 32 : share == LIN_SPLIT || p.bn < 64 ? p.bn : 64;
+    p.n_fblocks = is_pair(share) ? fb2 : fb;
+    p.box = DW ? 64 : is_pair(share) ? 32 : share == LIN_SPLIT || p.bn < 64 ? p.bn : 64;
 
     CUtensorMap ta, tb;
     const bool ok = DW ? make_map(&ta, a, K, p.rows, 0, 64) && make_map(&tb, b, N, p.rows, 0, 64)
                        : make_map(&ta, a, K, N, p.E, MODE == LIN_FWD ? 128 : 64) &&
                              make_map(&tb, b, p.C, p.rows, 0, p.box);
     if (!ok) return MOE_ERR_CUDA;
-    auto kernel = share == LIN_PAIR    ? linear_kernel<MODE, LIN_PAIR>
-                  : share == LIN_SPLIT ? linear_kernel<MODE, LIN_SPLIT>
-                                       : linear_kernel<MODE, LIN_ONE>;
+    auto kernel = share == LIN_PAIR         ? linear_kernel<MODE, LIN_PAIR>
+                  : share == LIN_PAIR_SPLIT ? linear_kernel<MODE, LIN_PAIR_SPLIT>
+                  : share == LIN_SPLIT      ? linear_kernel<MODE, LIN_SPLIT>
+                                            : linear_kernel<MODE, LIN_ONE>;
     if (allow_max_smem(kernel) != MOE_OK || prefer_smem(kernel) != MOE_OK) return MOE_ERR_CUDA;
     const int64_t tiles = n_units * p.n_fblocks;
-    const int64_t grid = share == LIN_SPLIT ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
+    const int64_t grid = is_split(share) ? tiles : tiles < sms / cluster ? tiles : sms / cluster;
     return launch_cluster(kernel, unsigned(grid * cluster), LN_THREADS, size_t(smem), unsigned(cluster), stream, ta, tb, p);
 }
 

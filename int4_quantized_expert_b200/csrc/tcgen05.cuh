@@ -14,8 +14,8 @@
 namespace moe {
 
 // PAIR (here and below): cta_group::2, the two CTAs of a cluster working as
-// one.  Both allocate and free together; one thread of the CTA of rank 0
-// issues the MMAs, which read both CTAs' shared memory at the same offsets (A:
+// one (ranks 2 i and 2 i + 1 of a cluster).  Both allocate and free together; one
+// thread of the CTA of even rank issues the MMAs, which read both CTAs' shared memory at the same offsets (A:
 // each CTA's half of the M rows; B: each CTA's half of the N columns) and
 // write each CTA's half of the rows to its tensor memory.
 template <bool PAIR = false>
@@ -100,10 +100,11 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
                  :: "r"(smem_u32(bar)) : "memory");
 }
 
-// the same for a pair's MMAs, on the barriers at this offset in both CTAs
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+// the same for a pair's MMAs, on the barriers at this offset in the CTAs of the
+// cluster that have their bit in `ctas`
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar, uint32_t ctas) {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-                 :: "r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+                 :: "r"(smem_u32(bar)), "h"(uint16_t(ctas)) : "memory");
 }
 
 // 32 consecutive columns of this thread's lane, then wait for the load.

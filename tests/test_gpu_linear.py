@@ -114,6 +114,17 @@ def test_linear_pairs_sizes(T, K, N):
     backward_case(T, K, N, "relu", torch.float32, seed=15)
 
 
+# tiles of 256 features whose contraction is split over two to four pairs of CTAs
+@pytest.mark.parametrize("T,K,N", [(224, 4104, 3592), (256, 5120, 5120), (480, 5128, 2056), (700, 4104, 1544), (511, 1544, 264)])
+def test_linear_forward_split_pairs(T, K, N):
+    forward_case(T, K, N, "gelu", True, True, True, seed=19)
+
+
+@pytest.mark.parametrize("T,K,N,act", [(250, 3080, 4104, "silu"), (8187, 1024, 1000, "relu"), (300, 520, 4104, "none")])
+def test_linear_backward_split_pairs(T, K, N, act):
+    backward_case(T, K, N, act, torch.bfloat16 if T < 400 else torch.float32, seed=20)
+
+
 def test_linear_residual_in_place_and_repeat_calls():
     for T, K, N in ((5, 1024, 512), (700, 256, 520)):
         x, w, r = rnd(1, T, K).cuda(), rnd(2, N, K, std=K ** -0.5).cuda(), rnd(3, T, N).cuda()
@@ -435,7 +446,8 @@ def test_waits_time_out_then_the_next_call_recovers():
     x, w = rnd(1, 300, 520).cuda(), rnd(2, 264, 520).cuda()
     one, wide = rnd(3, 1, 4096).cuda(), rnd(4, 128, 4096).cuda()
     dy = rnd(5, 300, 264).cuda()
-    calls = [lambda: [moe.linear(x, w)], lambda: [moe.linear(one, wide)],
+    few, square = rnd(6, 256, 4096).cuda(), rnd(7, 3840, 4096).cuda()
+    calls = [lambda: [moe.linear(x, w)], lambda: [moe.linear(one, wide)], lambda: [moe.linear(few, square)],
              lambda: [t for t in moe.linear_backward(dy, x, w)[:2]]]
     for call in calls:
         want = call()
