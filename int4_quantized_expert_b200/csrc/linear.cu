@@ -1037,25 +1037,31 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
         }
     }
     for (int bn = DW || (p.offsets && p.rows > 64) ? 64 : 16; bn <= 192; bn += DW ? 64 : 16) {
-        const int64_t tiles = units(bn) * fb;
+        const int64_t all = units(bn) * fb;
+        if (all > 8 * sms) {
+            if (bn >= cols) break;
+            continue;
+        }
+        const int tiles = int(all);
         // as many CTAs to a tile as two to an SM or one to an SM allow, or one;
         // wider than 128, a tile that is not split is a pair's or another kernel's
-        for (int per_sm = bn <= 64 ? 2 : 1; tiles <= sms && per_sm >= 0; --per_sm) {
-            int s = per_sm ? int(per_sm * sms / tiles) : 1;
+        for (int per_sm = bn <= 64 ? 2 : 1, last = 0; tiles <= sms && per_sm >= 0; --per_sm) {
+            int s = per_sm ? per_sm * sms / tiles : 1;
             if (s > 8) s = 8;
             if (s > steps) s = steps;
             while (s > 1 && (bn <= 64 ? 2 : 1) * max_clusters(s) < tiles) --s;
-            if (s == 1 && bn > 128) continue;
+            if (s == last || (s == 1 && bn > 128)) continue;
+            last = s;
             const bool shared_sms = s * tiles > sms;
             const int load = (shared_sms ? 2 : 1) * (256 + 2 * bn);
-            const int64_t time = loop(ceil_div(steps, s) * (load < 480 ? 480 : load), shared_sms) +
+            const int64_t time = loop(int64_t((steps + s - 1) / s) * (load < 480 ? 480 : load), shared_sms) +
                                  (column + 50 / s) * bn + (s > 1 ? 5000 + 150 * s : 2500);
             if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = s;
         }
         // more tiles than SMs, two CTAs to an SM: one's epilogue under the other's loads
-        if (bn <= 64 && tiles > sms && tiles <= 8 * sms) {
+        if (bn <= 64 && tiles > sms) {
             const int load = 2 * (256 + 2 * bn);
-            const int64_t time = loop(ceil_div(tiles, 2 * sms) * (int64_t(steps) * (load < 480 ? 480 : load) + (column + 50) * bn + 2500),
+            const int64_t time = loop((tiles + 2 * sms - 1) / (2 * sms) * (int64_t(steps) * (load < 480 ? 480 : load) + (column + 50) * bn + 2500),
                                       true) + 2500;
             if (time < best) best = time, share = LIN_SPLIT, p.bn = bn, p.split = 1;
         }

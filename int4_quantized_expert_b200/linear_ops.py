@@ -27,11 +27,12 @@ _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 # once, and the stream's handle is taken without building a Stream object
 # (14.2 -> 8.7 us for a call of linear, of which 3.7 are the library's).
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice   # the tensors of a call are on a device already
 
 
 def _elsewhere(index: int, stream) -> bool:
     """Whether ``stream`` or the device ``index`` of the tensors has to be made current first."""
-    return stream is not None or index != torch.cuda.current_device()
+    return stream is not None or index != _current_device()
 
 
 @contextlib.contextmanager
