@@ -12,6 +12,10 @@ Tolerances (derived, per element).  S is the sum of the products' magnitudes.
         neighbour, one bf16 step away, is as right: that step's products are
         added to the bound.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -461,3 +465,55 @@ def test_waits_time_out_then_the_next_call_recovers():
         got = call()
         assert moe.linear_device_status() == moe.Status.OK
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_offsets_past_32_bits():
+    """A weight of 2^32 values: rows far into w, dx's sums over them, and dw's far rows."""
+    T, K, N = 24, 65536, 65536
+    g = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s, std=1.0: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(0.0, std, generator=g)
+    x, w, dy = r(T, K), r(N, K, std=K ** -0.5), r(T, N)
+    rows = [0, 1, 32767, 32768, 40000, 65534, 65535]
+    y = moe.linear(x, w)
+    dx, dw, _ = moe.linear_backward(dy, x, w)
+    assert moe.linear_device_status() == moe.Status.OK
+    check(y[:, rows], f64(x) @ f64(w[rows]).T, sum_tol(K, np.abs(f64(x)) @ np.abs(f64(w[rows])).T))
+    check(dw[rows], f64(dy[:, rows]).T @ f64(x), sum_tol(T, np.abs(f64(dy[:, rows])).T @ np.abs(f64(x))))
+    cols = [0, 7, 32768, 65535]
+    check(dx[:, cols], f64(dy) @ f64(w[:, cols]), sum_tol(N, np.abs(f64(dy)) @ np.abs(f64(w[:, cols]))))
+
+
+@pytest.mark.parametrize("K,N", [(8, 16), (136, 8)])
+def test_the_most_rows(K, N):
+    T = 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s, std=1.0: torch.empty(*s, dtype=torch.bfloat16, device="cuda").normal_(0.0, std, generator=g)
+    x, w, dy = r(T, K), r(N, K), r(T, N)
+    y = moe.linear(x, w)
+    dx, dw, db = moe.linear_backward(dy, x, w, need_dbias=True, grad_dtype=torch.float32)
+    assert moe.linear_device_status() == moe.Status.OK
+    x, w, dy = (t.double() for t in (x, w, dy))
+    for got, ref, S, C in ((y, x @ w.T, x.abs() @ w.abs().T, K), (dx, dy @ w, dy.abs() @ w.abs(), N),
+                           (dw, dy.T @ x, dy.abs().T @ x.abs(), T), (db, dy.sum(0), dy.abs().sum(0), T)):
+        u = U[got.dtype]
+        tol = sum_tol(C, S)
+        assert ((got.double() - ref).abs() <= u * (ref.abs() + tol) + tol).all()
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = """
+import torch, int4_quantized_expert_b200 as moe
+bf = dict(dtype=torch.bfloat16, device="cuda")
+x, w, dy = torch.ones(300, 2048, **bf), torch.ones(3600, 2048, **bf), torch.ones(300, 3600, **bf)
+one, off = torch.ones(1, 2048, **bf), torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    y, t = moe.linear(x, w), moe.linear(one, w, activation=moe.ACT_RELU)
+    dx, dw, db = moe.linear_backward(dy, x, w, activation=moe.ACT_GELU, preact=dy, need_dbias=True)
+    z = moe.grouped_linear(x, w.view(2, 1800, 2048), off)
+    h = moe.swiglu(y)
+g.replay()
+assert moe.linear_device_status() == 0
+assert (y == 2048).all() and (t == 2048).all() and (z == 2048).all() and (h > 1e6).all() and dw.isfinite().all()
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=os.path.dirname(os.path.dirname(__file__)))
