@@ -1016,10 +1016,11 @@ moe_status launch_mode(const bf16* a, const bf16* b, int32_t N, int32_t K, LinPa
     };
     int64_t best = rounds(ceil_div(units(p.bn) * fb, sms), steps * int64_t(p.bn < 112 ? 480 : 256 + 2 * p.bn),
                           column * p.bn) + 4000;
-    if (cols > 128) {
+    // (experts of fewer rows on average too: some have more)
+    if (cols > (p.offsets && !DW ? 64 : 128)) {
         p.chunks = DW || p.offsets ? 0 : pair_chunks(p.rows, fb2, steps, sms / 2);
         const int64_t n = p.chunks ? p.chunks : units(256), width = p.chunks ? (ceil_div(p.rows, p.chunks) + 31) & ~31 : 256;
-        const int64_t step = width > 256 ? 2 * width : width < 224 ? 480 : 256 + width;
+        const int64_t step = width > 256 ? 2 * width : width < 224 || cols < 224 ? 480 : 256 + width;
         const int64_t time = rounds(ceil_div(n * fb2, sms / 2), steps * step, column * width) + 4500;
         if (time < best) best = time, share = LIN_PAIR;
     }
