@@ -930,6 +930,7 @@ int pair_chunks(int rows, int n_fblocks, int steps, int pairs) {
     int64_t best_time = INT64_MAX;
     for (int c = least; c <= most; ++c) {
         const int n = (int(ceil_div(rows, c)) + 31) & ~31;
+        if ((c - 1) * n >= rows) continue;   // no chunk may be empty
         const int64_t tile = int64_t(steps) * (n > 256 ? 2 * n : n < 224 ? 480 : n + 256) + (n > 256 ? 5000 : 0);
         const int64_t time = ceil_div(int64_t(c) * n_fblocks, pairs) * tile;
         if (time < best_time) best = c, best_time = time;
