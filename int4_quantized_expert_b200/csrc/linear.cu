@@ -16,9 +16,9 @@
 // Tiles: 128 features x up to bn columns, steps of 64 along c, through a ring
 // of TMA-filled slots (A 16 KB, B bn x 128 B, 128-byte swizzle).  D is fp32 in
 // tensor memory, whose 512 columns are handed out in turn, so a tile's epilogue
-// overlaps the next tile's MMAs.  TMA's zero fill pads c, features and rows at the tensors'
-// edges; what it cannot pad is the end of an expert's rows inside the tensor
-// when c runs over rows (LIN_DW): warp 2 zeroes those rows of both operands
+// overlaps the next tile's MMAs.  TMA's zero fill pads c, features and rows at
+// the tensors' edges; what it cannot pad is the end of an expert's rows inside the
+// tensor when c runs over rows (LIN_DW): warp 2 zeroes those rows of both operands
 // in the slot before the MMAs read it, so rows of the next expert -- which may
 // hold NaN -- never enter.
 //
@@ -30,26 +30,26 @@
 // the same MMAs.
 //
 // An expert's rows are cut into equal chunks of at most bn rows (rounded up to
-// 16), not into full chunks and a tail: a tail of a few rows would stream a
-// whole weight tile for them.  A pair's tile may have up to 320 rows, as two
-// accumulators (192 columns and the rest) under one pass over the weights: 300
-// rows in two tiles of 160 would load the weights twice, and the 64 bytes a
-// cycle that an SM can load are what bounds narrow tiles.  Each CTA derives the list from the offsets by a
-// scan over the (at most 256) experts.
+// 16, pairs: 32), not into full chunks and a tail: a tail of a few rows would
+// stream a whole weight tile for them.  A pair's tile may have up to 320 rows, as
+// two accumulators (192 columns and the rest) under one pass over the weights: 300
+// rows in two tiles of 160 would load the weights twice, and the 64 bytes a cycle
+// that an SM can load are what bounds narrow tiles.  Each CTA derives the list from
+// the offsets by a scan over the (at most 256) experts.
 //
 // LIN_PAIR_SPLIT: where there are few such tiles, two to four pairs of a cluster
 // share one's contraction, as in LIN_SPLIT below; their rings take the sums once all
 // are past their MMAs.
 //
-// LIN_SPLIT: when the tiles fit the SMs at once, a CTA takes one tile of up to
-// 128 columns, or a cluster of up to 8 CTAs shares the contraction of one of up to
-// 192 and each finishes a part of the tile.  Partial sums are sent to the CTA that finishes
-// them (st.async to its shared memory, counted by a barrier there) and added in
-// rank order: no scratch, no atomics, the same bits every time.  Short calls are
-// bound by latency or by the weights' bytes, so what counts is how soon a call's
-// loads follow the last call's: where half of an SM's shared memory is enough, the
-// next call's CTAs (programmatic dependent launch) are set up and waiting beside
-// this one's.
+// LIN_SPLIT: when there are few tiles, a CTA takes one of up to 128 columns, or a
+// cluster of up to 8 CTAs shares the contraction of one of up to 192 and each
+// finishes a part of the tile.  Partial sums are sent to the CTA that finishes them
+// (st.async to its shared memory, counted by a barrier there; its own are plain
+// stores) and added in rank order: no scratch, no atomics, the same bits every
+// time.  Short calls are bound by latency or by the weights' bytes, so what counts
+// is how soon a call's loads follow the last call's: where half of an SM's shared
+// memory is enough, the next call's CTAs (programmatic dependent launch) are set up
+// and waiting beside this one's.
 //
 // Without offsets, a CTA knows its weights before it has waited for the kernel
 // before it, and asks for a ring's worth of them to be brought into L2.

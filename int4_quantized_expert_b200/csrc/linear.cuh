@@ -20,13 +20,13 @@ struct LinParams {
     int32_t C;                // contraction length: K, N, (rows of the expert)
     int32_t NC;               // LIN_DW: columns N
     int32_t n_fblocks;        // ceil(F / 128)
-    int32_t bn;               // most columns of a tile: 16, 32, 64, 128, 256 or 320
+    int32_t bn;               // most columns of a tile: 16 to 320
     int32_t chunks;           // chunks of the rows when there are no offsets
     int32_t box;              // rows of a TMA box of B (LIN_DW: 64 columns n of each of 64 rows)
     int32_t stages;           // slots of the operand ring
     int32_t ring_bytes;       // its size
     int32_t tmem_cols;        // tensor memory columns
-    int32_t split;            // CTAs of a cluster that share a tile's contraction
+    int32_t split;            // CTAs (pairs) of a cluster that share a tile's contraction
     void* out;
     int32_t out_fp32;
     int32_t act;              // moe_activation (LIN_FWD)
