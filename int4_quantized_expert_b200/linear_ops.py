@@ -25,7 +25,7 @@ _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 # What the calls of a decode step pay on the host before their kernel starts
 # counts as much as the kernel: the checks below read each property of a tensor
 # once, and the stream's handle is taken without building a Stream object
-# (14.2 -> 8.7 us for a call of linear, of which 3.7 are the library's).
+# (14.2 -> 8.7 us for a call of linear, of which 3.9 are the library's).
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice   # the tensors of a call are on a device already
 
@@ -67,6 +67,14 @@ def _matrix(name: str, t: torch.Tensor, dims: int = 2) -> torch.Size:
     return t.shape
 
 
+def _sizes(x: torch.Tensor, w: torch.Tensor) -> tuple:
+    """(T, K, N, device index) of ``x[T, K]`` and ``w[N, ...]``."""
+    if x.dim() != 2 or w.dim() != 2 or not x.is_cuda:
+        _matrix("x", x), _matrix("w", w)   # one of them raises
+    T, K = x.shape
+    return T, K, w.shape[0], x.get_device()
+
+
 def _dtype(dtype: torch.dtype) -> int:
     if dtype not in _DTYPES:
         raise ValueError("the output type must be torch.bfloat16 or torch.float32")
@@ -79,8 +87,8 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     """``y = act(x w^T + bias) + residual`` for bf16 ``x[T, K]``, ``w[N, K]``, ``bias[N]``,
     ``residual[T, N]`` (see ``moe_linear_forward``).  ``out`` may be the residual itself.  With
     ``save_preact`` the result is ``(y, z)``, z the rounded pre-activations ``linear_backward`` takes."""
-    (T, K), (N, _) = _matrix("x", x), _matrix("w", w)
-    at, bf = x.get_device(), torch.bfloat16
+    T, K, N, at = _sizes(x, w)
+    bf = torch.bfloat16
     if _elsewhere(at, stream):
         with _on(at, stream):
             return linear(x, w, bias, activation=activation, residual=residual, save_preact=save_preact, out=out)
@@ -106,8 +114,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, activ
     place of a gradient that is not wanted.  ``preact`` is the z that ``linear(save_preact=True)``
     returned (not needed without an activation); ``grad_dtype`` is the type of dw and dbias.  The
     residual's gradient is ``dy``."""
-    (T, K), (N, _) = _matrix("x", x), _matrix("w", w)
-    at, bf, gt = x.get_device(), torch.bfloat16, _dtype(grad_dtype)
+    T, K, N, at = _sizes(x, w)
+    bf, gt = torch.bfloat16, _dtype(grad_dtype)
     if _elsewhere(at, stream):
         with _on(at, stream):
             return linear_backward(dy, x, w, activation=activation, preact=preact, need_dx=need_dx, need_dw=need_dw,
