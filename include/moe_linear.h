@@ -86,9 +86,9 @@ MOE_API moe_status moe_linear_backward(const void* dy, const void* x, int32_t T,
  *            moe_route writes them.  Experts may be empty.
  *   y  [n, N] of y_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_FP32); rows before
  *      offsets[0] and from offsets[E] on are left as they were.
- * An expert whose two offsets are out of order or out of range is taken as
- * empty and reported by moe_linear_device_status; where the ranges that are left
- * overlap, their rows' results are unspecified.
+ * An expert whose two offsets are out of order or out of range, or whose range
+ * overlaps an earlier expert's, is taken as empty and reported by
+ * moe_linear_device_status; the other experts' results are as ever.
  * Requires 0 <= n <= 1048576; 1 <= E <= 256; K and N multiples of 8 in
  * [8, 65536].
  */

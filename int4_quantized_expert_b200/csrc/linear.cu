@@ -136,6 +136,11 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (512ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// Whether an expert's two offsets are a range of the rows.
+__device__ __forceinline__ bool in_order(int begin, int end, int rows) {
+    return begin >= 0 && end >= begin && end <= rows;
+}
+
 // Chunks of an expert's rows.  Tiles of up to 320 rows save a pass over the
 // weights where few chunks of up to 256 would be narrow.
 __device__ __forceinline__ int row_chunks(int rows, int bn) {
@@ -386,22 +391,34 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     if (p.offsets) griddep_wait();
 
     // the row ranges, and for LIN_FWD / LIN_DX the chunks before each expert
-    int chunks = 0;
+    int chunks = 0, begin = 0, count = 0;
     if (int(threadIdx.x) < p.E) {
-        int b = 0, c = p.rows;
+        count = p.rows;
         if (p.offsets) {
-            b = p.offsets[threadIdx.x];
+            begin = p.offsets[threadIdx.x];
             const int end = p.offsets[threadIdx.x + 1];
-            if (b >= 0 && end >= b && end <= p.rows) {
-                c = end - b;
-            } else {
-                b = c = 0;
+            count = in_order(begin, end, p.rows) ? end - begin : -1;
+        }
+    }
+    // Where two offsets are out of order, ranges that are in order by themselves may
+    // overlap.  Those that overlap an earlier one count as empty too: a grid of split
+    // tiles has room for the chunks of ranges that are apart and no more.
+    if (p.offsets && __syncthreads_or(count < 0)) {
+        if (int(threadIdx.x) < p.E) {
+            for (int i = 0; count > 0 && i < int(threadIdx.x); ++i) {
+                const int b = p.offsets[i], end = p.offsets[i + 1];
+                if (in_order(b, end, p.rows) && max(b, begin) < min(end, begin + count)) count = -1;
+            }
+            if (count < 0) {
+                begin = count = 0;
                 if (blockIdx.x == 0) atomicOr(&g_linear_status, DEV_BAD_EXPERT);
             }
         }
-        sm->begin[threadIdx.x] = b;
-        sm->count[threadIdx.x] = c;
-        chunks = p.offsets ? row_chunks(c, p.bn) : p.chunks;
+    }
+    if (int(threadIdx.x) < p.E) {
+        sm->begin[threadIdx.x] = begin;
+        sm->count[threadIdx.x] = count;
+        chunks = p.offsets ? row_chunks(count, p.bn) : p.chunks;
     }
     if (MODE != LIN_DW) {
         int incl = chunks;

@@ -1,0 +1,64 @@
+"""The linear, grouped and SwiGLU operators where callers or values go astray:
+offsets out of order, reports from several streams, the activations' far ends.
+Tolerances as derived in test_gpu_linear.py."""
+import numpy as np
+import pytest
+import torch
+
+import int4_quantized_expert_b200 as moe
+from oracle import linear as ol
+from tests.test_gpu_linear import check, f64, rnd, sum_tol
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------
+# offsets out of order
+# ---------------------------------------------------------------------------
+def kept_ranges(off, n):
+    """(begin, end) of each expert's rows; (0, 0) where the two offsets are no range of the rows, or
+    one that overlaps an earlier range."""
+    ranges = [(a, b) if 0 <= a <= b <= n else (0, 0) for a, b in zip(off, off[1:])]
+    return [(a, b) if all(max(a, c) >= min(b, d) for c, d in ranges[:e]) else (0, 0) for e, (a, b) in enumerate(ranges)]
+
+
+def overlapping_case(off, n, K, N):
+    E, ranges = len(off) - 1, kept_ranges(off, n)
+    x, w, dy = rnd(1, n, K), rnd(2, E, N, K, std=K ** -0.5), rnd(3, n, N)
+    oc = torch.tensor(off, dtype=torch.int32, device="cuda")
+    y = torch.full((n, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    dx = torch.full((n, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert moe.linear_device_status() == moe.Status.OK
+    moe.grouped_linear(x.cuda(), w.cuda(), oc, out=y)
+    assert moe.linear_device_status() == moe.Status.INVALID_ARG
+    _, dw = moe.grouped_linear_backward(dy.cuda(), x.cuda(), w.cuda(), oc, dx=dx)
+    assert moe.linear_device_status() == moe.Status.INVALID_ARG
+    fx, fw, fdy = f64(x), f64(w), f64(dy)
+    free = np.ones(n, bool)
+    for e, (a, b) in enumerate(ranges):
+        s = slice(a, b)
+        free[s] = False
+        check(y[s], fx[s] @ fw[e].T, sum_tol(K, np.abs(fx[s]) @ np.abs(fw[e]).T))
+        check(dx[s], fdy[s] @ fw[e], sum_tol(N, np.abs(fdy[s]) @ np.abs(fw[e])))
+        check(dw[e], fdy[s].T @ fx[s], sum_tol(b - a, np.abs(fdy[s]).T @ np.abs(fx[s])))
+    free = torch.from_numpy(free).cuda()
+    assert (y[free] == 7).all() and (dx[free] == 7).all()      # rows of no expert are left as they were
+
+
+# Tiles whose contraction is split have a grid of as many as ranges that are apart
+# can need: repeated ranges must not push the last expert's tiles out of it.
+@pytest.mark.parametrize("off,n", [([0, 600, 0, 600, 640, 640], 640), ([0, 600, 0, 600, 0, 600, 640], 640),
+                                   ([0, 48] * 8 + [48, 64], 64), ([0, 60] * 30 + [60, 64], 64),
+                                   ([30, 64, 0, 30, 20, 64], 64), ([0, 128, 64, 192, 128, 256, 250, 300], 300),
+                                   ([0, 9000, 0, 9000, 8000, 9001], 9001)])
+@pytest.mark.parametrize("K,N", [(2056, 136), (136, 1032)])
+def test_grouped_overlapping_ranges(off, n, K, N):
+    if n > 1000:
+        K, N = min(K, 264), min(N, 264)
+    overlapping_case(off, n, K, N)
+
+
+@pytest.mark.parametrize("off", [[0, 20, 10, 40, 64], [-5, 20, 20, 40, 64], [0, 20, 20, 40, 65], [64, 0, 64, 0, 64],
+                                 [0, 20, 20, 40, 2 ** 31 - 1], [0, 20, 20, 40, -2 ** 31], [-2 ** 31, 2 ** 31 - 1, 0, 5, 64]])
+def test_grouped_bad_offsets_row_by_row(off):
+    overlapping_case(off, 64, 32, 48)
