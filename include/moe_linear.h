@@ -127,11 +127,13 @@ MOE_API moe_status moe_swiglu_backward(const void* dh, const void* gu, int32_t n
  * moe_linear_device_status -- SYNCHRONIZES `stream`, then returns what the
  * kernels behind moe_linear_* and moe_grouped_linear_* reported on the
  * current device since the last such query, and clears it: MOE_OK,
- * MOE_ERR_TIMEOUT (a bounded device wait gave up; outputs are invalid),
- * MOE_ERR_INVALID_ARG (offsets out of order or out of range) or
- * MOE_ERR_CUDA.  One status word per device serves every stream; it lives in
- * the library, so nothing has to be passed or cleared.  Not to be called
- * while `stream` is being captured.
+ * MOE_ERR_TIMEOUT (a bounded device wait gave up; outputs are invalid; also
+ * where offsets were reported as well), MOE_ERR_INVALID_ARG (offsets out of
+ * order or out of range, or ranges that overlap) or MOE_ERR_CUDA.  One status
+ * word per device serves every stream: a query takes what any stream reported,
+ * and of queries at the same time one gets a report.  It lives in the library,
+ * so nothing has to be passed or cleared.  Not to be called while `stream` is
+ * being captured.
  */
 MOE_API moe_status moe_linear_device_status(void* stream);
 

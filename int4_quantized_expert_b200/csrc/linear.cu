@@ -91,6 +91,11 @@ constexpr int LN_STG_BYTES = 32 * 64;     // an epilogue warp's staging buffer: 
 // What the kernels report (moe_linear_device_status): DEV_* values or-ed into one word per device.
 static __device__ int32_t g_linear_status;
 
+// What a query has taken from it.  Reading and clearing are one step: kernels of
+// other streams report, and other threads query, at any time between two steps.
+static __device__ int32_t g_linear_taken;
+static __global__ void take_status_kernel() { g_linear_taken = atomicExch(&g_linear_status, DEV_OK); }
+
 // How CTAs share tiles: one tile each, a cluster per tile along the contraction,
 // two CTAs per tile of 256 features, or a cluster of pairs per such tile.
 enum LinShare { LIN_ONE, LIN_SPLIT, LIN_PAIR, LIN_PAIR_SPLIT };
@@ -1171,15 +1176,16 @@ moe_status set_wait_limit_linear(uint32_t cycles) {
 }
 
 moe_status linear_device_status(cudaStream_t stream) {
+    static std::mutex mu;   // g_linear_taken belongs to one query at a time
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;   // not under the lock
+    std::lock_guard<std::mutex> lock(mu);
+    take_status_kernel<<<1, 1, 0, stream>>>();
     int32_t v = 0;
-    const int32_t zero = 0;
-    if (cudaMemcpyFromSymbolAsync(&v, g_linear_status, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+    if (launch_status() != MOE_OK ||
+        cudaMemcpyFromSymbolAsync(&v, g_linear_taken, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
         cudaStreamSynchronize(stream) != cudaSuccess)
         return MOE_ERR_CUDA;
     if (v == DEV_OK) return MOE_OK;
-    if (cudaMemcpyToSymbolAsync(g_linear_status, &zero, sizeof(zero), 0, cudaMemcpyHostToDevice, stream) != cudaSuccess ||
-        cudaStreamSynchronize(stream) != cudaSuccess)
-        return MOE_ERR_CUDA;
     return v & DEV_TIMEOUT ? MOE_ERR_TIMEOUT : MOE_ERR_INVALID_ARG;
 }
 

@@ -48,7 +48,7 @@ moe_status launch_swiglu_backward(const bf16* dh, const bf16* gu, int32_t n, int
                                   cudaStream_t stream);
 
 moe_status set_wait_limit_linear(uint32_t cycles);
-// Reads and clears the current device's status word (synchronizes `stream`).
+// Takes the current device's status word, leaving it clear (synchronizes `stream`).
 moe_status linear_device_status(cudaStream_t stream);
 
 }  // namespace moe

@@ -1,6 +1,8 @@
 """The linear, grouped and SwiGLU operators where callers or values go astray:
 offsets out of order, reports from several streams, the activations' far ends.
 Tolerances as derived in test_gpu_linear.py."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -62,3 +64,42 @@ def test_grouped_overlapping_ranges(off, n, K, N):
                                  [0, 20, 20, 40, 2 ** 31 - 1], [0, 20, 20, 40, -2 ** 31], [-2 ** 31, 2 ** 31 - 1, 0, 5, 64]])
 def test_grouped_bad_offsets_row_by_row(off):
     overlapping_case(off, 64, 32, 48)
+
+
+# ---------------------------------------------------------------------------
+# the status word
+# ---------------------------------------------------------------------------
+def test_each_report_is_taken_once():
+    """One thread makes a call that is reported, waits for it and queries; another queries all the
+    while on its own stream.  Each report is returned to exactly one of them: none is lost between
+    another query's reading and clearing, none is returned twice."""
+    x, w = rnd(1, 64, 32).cuda(), rnd(2, 2, 48, 32).cuda()
+    off = torch.tensor([0, 20, 65], dtype=torch.int32, device="cuda")     # one range past the rows: one report
+    y = torch.empty(64, 48, dtype=torch.bfloat16, device="cuda")
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert moe.linear_device_status() == moe.Status.OK
+    rounds, done, taken, wrong = 2000, threading.Event(), [0, 0], []
+
+    def query(who, stream):
+        s = moe.linear_device_status(stream)
+        taken[who] += s == moe.Status.INVALID_ARG
+        if s not in (moe.Status.OK, moe.Status.INVALID_ARG):
+            wrong.append(s)
+
+    def ask():
+        while not done.is_set():
+            query(1, other)
+
+    t = threading.Thread(target=ask)
+    t.start()
+    try:
+        for _ in range(rounds):
+            moe.grouped_linear(x, w, off, out=y, stream=mine)
+            mine.synchronize()
+            query(0, mine)
+    finally:
+        done.set()
+        t.join()
+    assert not wrong and sum(taken) == rounds, (taken, wrong)
+    assert moe.linear_device_status() == moe.Status.OK
