@@ -808,14 +808,17 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
 // the rows.  A thread sums its rows in fp32, the CTA its row lanes and the
 // cluster its CTAs in a fixed order.  4099 x 5120 with GELU: 24 us, 5.2 TB/s;
 // strips of 32 and 128 columns, 512 threads and two or eight rows in flight a
-// thread all took 28 to 37 us.
+// thread all took 28 to 37 us.  Five CTAs to an SM (48 registers) run these 640 at
+// once; left to itself the compiler takes 64 registers, and the last 48 CTAs run
+// alone: 33 us.
 // ---------------------------------------------------------------------------
 constexpr int AG_THREADS = 256, AG_SPLIT = 8, AG_COLS = 64, AG_ROWS = AG_THREADS * 8 / AG_COLS;
 
 template <bool DZ, bool DB>
-__global__ void __launch_bounds__(AG_THREADS) act_grad_kernel(const bf16* __restrict__ dy, const bf16* __restrict__ z,
-                                                              int T, int N, int act, bf16* __restrict__ dz,
-                                                              void* __restrict__ dbias, int dbias_fp32) {
+__global__ void __launch_bounds__(AG_THREADS, 5) act_grad_kernel(const bf16* __restrict__ dy,
+                                                                 const bf16* __restrict__ z, int T, int N, int act,
+                                                                 bf16* __restrict__ dz, void* __restrict__ dbias,
+                                                                 int dbias_fp32) {
     __shared__ float part[AG_ROWS][AG_COLS + 1];
     __shared__ float sums[AG_COLS];
     griddep_launch_dependents();

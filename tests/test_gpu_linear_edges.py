@@ -103,3 +103,42 @@ def test_each_report_is_taken_once():
         t.join()
     assert not wrong and sum(taken) == rounds, (taken, wrong)
     assert moe.linear_device_status() == moe.Status.OK
+
+
+# ---------------------------------------------------------------------------
+# the activations' far ends
+# ---------------------------------------------------------------------------
+def every_bf16(lo, hi):
+    """every bf16 value of magnitude lo .. hi, and its negative"""
+    v = torch.arange(2 ** 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v[(v.float() >= lo) & (v.float() <= hi)]
+    return torch.cat([v, -v])
+
+
+def through_slope(z, act):
+    """act'(z): the bias gradient in fp32 of one row of ones"""
+    n = -(-z.numel() // 8) * 8
+    row = torch.zeros(1, n, dtype=torch.bfloat16)
+    row[0, :z.numel()] = z
+    row = row.cuda()
+    _, _, db = moe.linear_backward(torch.ones_like(row), torch.zeros(1, 8, dtype=torch.bfloat16, device="cuda"),
+                                   torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda"), activation=act, preact=row,
+                                   need_dx=False, need_dw=False, need_dbias=True, grad_dtype=torch.float32)
+    return db[:z.numel()]
+
+
+def test_gelu_slope_everywhere():
+    """Within 3e-7, and in the negative tail within 3e-4 of itself (each from the fp32 evaluation of the
+    formula; 2^-20 and 2^-11 leave the hardware's powers and reciprocals their part); values below 2^-122 may
+    be flushed to 0 (a factor below 2^-126 is, times |z| < 16)."""
+    z = every_bf16(2.0 ** -20, 100.0)
+    got, want = f64(through_slope(z, moe.ACT_GELU)), ol.act_slope(f64(z), "gelu")
+    assert (np.abs(got - want) <= 2.0 ** -20).all()
+    tail = f64(z) < -1
+    assert (np.abs(got - want) <= 2.0 ** -11 * np.abs(want) + 2.0 ** -122)[tail].all()
+
+
+def test_gelu_slope_of_infinite_values():
+    inf, nan = float("inf"), float("nan")
+    got = through_slope(torch.tensor([inf, -inf, 3e38, -3e38, nan, 0.0, -0.0, 33.0, -33.0]).bfloat16(), moe.ACT_GELU)
+    assert got[[0, 2, 7]].eq(1).all() and got[[1, 3, 8]].eq(0).all() and got[4].isnan() and got[[5, 6]].eq(0.5).all()
