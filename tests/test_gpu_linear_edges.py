@@ -142,3 +142,30 @@ def test_gelu_slope_of_infinite_values():
     inf, nan = float("inf"), float("nan")
     got = through_slope(torch.tensor([inf, -inf, 3e38, -3e38, nan, 0.0, -0.0, 33.0, -33.0]).bfloat16(), moe.ACT_GELU)
     assert got[[0, 2, 7]].eq(1).all() and got[[1, 3, 8]].eq(0).all() and got[4].isnan() and got[[5, 6]].eq(0.5).all()
+
+
+def through_activation(z, act):
+    """act(z) of bf16 values, by a product with the unit matrix (exact: one product with 1, the rest 0)"""
+    x = torch.zeros(-(-z.numel() // 8), 8, dtype=torch.bfloat16)
+    x.view(-1)[:z.numel()] = z
+    return moe.linear(x.cuda(), torch.eye(8).bfloat16().cuda(), activation=act).view(-1)[:z.numel()]
+
+
+def test_gelu_everywhere():
+    """Within 2e-7 and 1.1e-3 of itself below -1 (the fit of Phi's logarithm in fp32; 2^-20 and 2^-9 leave the
+    hardware's powers their part) before the one rounding to bf16; values below 2^-122 may be flushed to 0 (a
+    factor below 2^-126 is, times |z| < 16)."""
+    z = every_bf16(2.0 ** -20, 100.0)
+    got, want = f64(through_activation(z, moe.ACT_GELU)), ol.act(f64(z), "gelu")
+    assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20).all()
+    tail = f64(z) < -1
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -9) * np.abs(want) + 2.0 ** -122)[tail].all()
+
+
+def test_gelu_of_infinite_values():
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([inf, -inf, nan, 3e38, -3e38]).bfloat16()
+    y = moe.linear(torch.ones(8, 8).bfloat16().cuda(), torch.zeros(8, 8).bfloat16().cuda(),
+                   torch.cat([z, torch.zeros(3).bfloat16()]).cuda(), activation=moe.ACT_GELU)
+    assert y[:, 0].eq(inf).all() and y[:, 1].eq(0).all() and y[:, 2].isnan().all()
+    assert y[:, 3].eq(z[3].item()).all() and y[:, 4].eq(0).all()
