@@ -25,14 +25,15 @@ _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 # What the calls of a decode step pay on the host before their kernel starts
 # counts as much as the kernel: the checks below read each property of a tensor
 # once, and the stream's handle is taken without building a Stream object
-# (14.2 -> 8.7 us for a call of linear, of which 3.9 are the library's).
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice   # the tensors of a call are on a device already
+# (14.2 -> 8.7 us for a call of linear, of which 3.9 are the library's).  What gives
+# it is looked up in a call, whose tensors are on a device already: a torch without
+# CUDA does not have it, and the package is imported there too.
+_C = torch._C
 
 
 def _elsewhere(index: int, stream) -> bool:
     """Whether ``stream`` or the device ``index`` of the tensors has to be made current first."""
-    return stream is not None or index != _current_device()
+    return stream is not None or index != _C._cuda_getDevice()
 
 
 @contextlib.contextmanager
@@ -103,7 +104,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     z = x.new_empty((T, N)) if save_preact else None
     _check("moe_linear_forward", lib().moe_linear_forward(
         px, T, K, pw, N, pb, activation, pr, None if z is None else z.data_ptr(),
-        pout, _raw_stream(at)))
+        pout, _C._cuda_getCurrentRawStream(at)))
     return (out, z) if save_preact else out
 
 
@@ -133,7 +134,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, activ
     db = x.new_empty((N,), dtype=grad_dtype) if need_dbias else None
     _check("moe_linear_backward", lib().moe_linear_backward(
         pdy, px, T, K, pw, N, activation, pz, *(None if t is None else t.data_ptr() for t in (dz, dx, dw, db)), gt,
-        _raw_stream(at)))
+        _C._cuda_getCurrentRawStream(at)))
     return dx, dw, db
 
 
@@ -161,7 +162,7 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
     else:
         pout = _tensor("out", out, (n, N), out_dtype, at)
     _check("moe_grouped_linear_forward", lib().moe_grouped_linear_forward(
-        px, n, K, pw, E, N, po, pout, yt, _raw_stream(at)))
+        px, n, K, pw, E, N, po, pout, yt, _C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -185,7 +186,7 @@ def grouped_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
         pdx = _tensor("dx", dx, (n, K), torch.bfloat16, at)
     dw = x.new_empty((E, N, K), dtype=grad_dtype) if need_dw else None
     _check("moe_grouped_linear_backward", lib().moe_grouped_linear_backward(
-        pdy, px, n, K, pw, E, N, po, pdx, None if dw is None else dw.data_ptr(), gt, _raw_stream(at)))
+        pdy, px, n, K, pw, E, N, po, pdx, None if dw is None else dw.data_ptr(), gt, _C._cuda_getCurrentRawStream(at)))
     return (dx if need_dx else None), dw
 
 
@@ -203,7 +204,7 @@ def swiglu(gu: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None)
     else:
         pout = _tensor("out", out, (n, F), bf, at)
     _check("moe_swiglu_forward", lib().moe_swiglu_forward(
-        pgu, n, F, pout, _raw_stream(at)))
+        pgu, n, F, pout, _C._cuda_getCurrentRawStream(at)))
     return out
 
 
@@ -222,7 +223,7 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, *, out: Optional[torch.T
     else:
         pout = _tensor("out", out, (n, F2), bf, at)
     _check("moe_swiglu_backward", lib().moe_swiglu_backward(
-        pdh, pgu, n, F, pout, _raw_stream(at)))
+        pdh, pgu, n, F, pout, _C._cuda_getCurrentRawStream(at)))
     return out
 
 

@@ -2,6 +2,8 @@
 ABI and the Python functions reject before touching a device."""
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -128,3 +130,19 @@ class _FakeCuda:
 def test_kernels_do_not_spill(src, kernels, tmp_path, monkeypatch):
     monkeypatch.setitem(resources.HOT, src, kernels)
     resources.test_hot_kernels_do_not_spill(src, tmp_path)
+
+
+def test_imports_without_cuda_bindings():
+    """A torch built without CUDA lacks the functions that give the current device and stream."""
+    code = """
+import torch
+del torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+import int4_quantized_expert_b200 as moe
+try:
+    moe.linear(torch.zeros(4, 16).bfloat16(), torch.zeros(24, 16).bfloat16())
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError("not refused")
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=ROOT)
