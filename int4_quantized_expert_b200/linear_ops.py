@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from . import DTYPE_BF16, DTYPE_FP32, _check, lib
+from . import DTYPE_BF16, DTYPE_FP32, MoEError, Status, _check, lib
 
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = range(4)
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
@@ -68,12 +68,20 @@ def _matrix(name: str, t: torch.Tensor, dims: int = 2) -> torch.Size:
     return t.shape
 
 
-def _sizes(x: torch.Tensor, w: torch.Tensor) -> tuple:
+def _too_large(fn: str) -> None:
+    """What the C ABI answers to sizes out of its range, for those that its 32-bit arguments cannot hold."""
+    raise MoEError(fn, Status.UNSUPPORTED_SHAPE)
+
+
+def _sizes(fn: str, x: torch.Tensor, w: torch.Tensor) -> tuple:
     """(T, K, N, device index) of ``x[T, K]`` and ``w[N, ...]``."""
     if x.dim() != 2 or w.dim() != 2 or not x.is_cuda:
         _matrix("x", x), _matrix("w", w)   # one of them raises
     T, K = x.shape
-    return T, K, w.shape[0], x.get_device()
+    N = w.shape[0]
+    if (T | K | N) >> 31:
+        _too_large(fn)
+    return T, K, N, x.get_device()
 
 
 def _dtype(dtype: torch.dtype) -> int:
@@ -88,7 +96,7 @@ def linear(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
     """``y = act(x w^T + bias) + residual`` for bf16 ``x[T, K]``, ``w[N, K]``, ``bias[N]``,
     ``residual[T, N]`` (see ``moe_linear_forward``).  ``out`` may be the residual itself.  With
     ``save_preact`` the result is ``(y, z)``, z the rounded pre-activations ``linear_backward`` takes."""
-    T, K, N, at = _sizes(x, w)
+    T, K, N, at = _sizes("moe_linear_forward", x, w)
     bf = torch.bfloat16
     if _elsewhere(at, stream):
         with _on(at, stream):
@@ -115,7 +123,7 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, activ
     place of a gradient that is not wanted.  ``preact`` is the z that ``linear(save_preact=True)``
     returned (not needed without an activation); ``grad_dtype`` is the type of dw and dbias.  The
     residual's gradient is ``dy``."""
-    T, K, N, at = _sizes(x, w)
+    T, K, N, at = _sizes("moe_linear_backward", x, w)
     bf, gt = torch.bfloat16, _dtype(grad_dtype)
     if _elsewhere(at, stream):
         with _on(at, stream):
@@ -138,8 +146,10 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, *, activ
     return dx, dw, db
 
 
-def _grouped(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, at: int):
+def _grouped(fn: str, x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, at: int):
     (n, K), (E, N, _) = x.shape, w.shape
+    if (n | K | E | N) >> 31:
+        _too_large(fn)
     return (n, K, E, N, _tensor("x", x, (n, K), torch.bfloat16, at), _tensor("w", w, (E, N, K), torch.bfloat16, at),
             _tensor("offsets", offsets, (E + 1,), torch.int32, at))
 
@@ -155,7 +165,7 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *,
     if _elsewhere(at, stream):
         with _on(at, stream):
             return grouped_linear(x, w, offsets, out_dtype=out_dtype, out=out)
-    n, K, E, N, px, pw, po = _grouped(x, w, offsets, at)
+    n, K, E, N, px, pw, po = _grouped("moe_grouped_linear_forward", x, w, offsets, at)
     if out is None:
         out = x.new_empty((n, N), dtype=out_dtype)
         pout = out.data_ptr()
@@ -178,7 +188,7 @@ def grouped_linear_backward(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, 
         with _on(at, stream):
             return grouped_linear_backward(dy, x, w, offsets, need_dx=need_dx, need_dw=need_dw, grad_dtype=grad_dtype,
                                            dx=dx)
-    n, K, E, N, px, pw, po = _grouped(x, w, offsets, at)
+    n, K, E, N, px, pw, po = _grouped("moe_grouped_linear_backward", x, w, offsets, at)
     pdy, pdx = _tensor("dy", dy, (n, N), torch.bfloat16, at), None
     if need_dx:
         if dx is None:
@@ -194,6 +204,8 @@ def swiglu(gu: torch.Tensor, *, out: Optional[torch.Tensor] = None, stream=None)
     """``h = silu(g) u`` for bf16 rows ``gu[n, 2F] = [g | u]`` (see ``moe_swiglu_forward``)."""
     n, F2 = _matrix("gu", gu)
     at, bf, F = gu.get_device(), torch.bfloat16, F2 // 2
+    if (n | F) >> 31:
+        _too_large("moe_swiglu_forward")
     if _elsewhere(at, stream):
         with _on(at, stream):
             return swiglu(gu, out=out)
@@ -213,6 +225,8 @@ def swiglu_backward(dh: torch.Tensor, gu: torch.Tensor, *, out: Optional[torch.T
     """``dgu = [dg | du]`` of ``swiglu`` from bf16 ``dh[n, F]`` (see ``moe_swiglu_backward``)."""
     n, F2 = _matrix("gu", gu)
     at, bf, F = gu.get_device(), torch.bfloat16, F2 // 2
+    if (n | F) >> 31:
+        _too_large("moe_swiglu_backward")
     if _elsewhere(at, stream):
         with _on(at, stream):
             return swiglu_backward(dh, gu, out=out)

@@ -146,3 +146,51 @@ else:
     raise AssertionError("not refused")
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=ROOT)
+
+
+class _Huge:
+    """What the functions ask of a CUDA tensor, with any shape and no memory behind it."""
+
+    is_cuda = True
+    device = torch.device("cuda", 0)
+
+    def __init__(self, *shape, dtype=torch.bfloat16):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def dim(self):
+        return len(self.shape)
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A[0]
+
+    def new_empty(self, shape, dtype=None):
+        return _Huge(*shape, dtype=dtype or self.dtype)
+
+
+def test_sizes_that_do_not_fit_the_abi(lib, monkeypatch):
+    """Rows or widths of 2^31 and more are refused, not taken modulo 2^32: 2^32 + 5 rows are not five."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    W = 1 << 32
+    off = _Huge(3, dtype=torch.int32)
+    calls = []
+    for t, k, n in ((W + 5, 16, 24), (5, W + 16, 24), (5, 16, W + 24), (1 << 31, 16, 24)):
+        x, w, dy = _Huge(t, k), _Huge(n, k), _Huge(t, n)
+        xs, ws = _Huge(t, k), _Huge(2, n, k)
+        calls += [lambda x=x, w=w: moe.linear(x, w), lambda x=x, w=w, dy=dy: moe.linear_backward(dy, x, w),
+                  lambda xs=xs, ws=ws: moe.grouped_linear(xs, ws, off),
+                  lambda xs=xs, ws=ws, dy=dy: moe.grouped_linear_backward(dy, xs, ws, off)]
+    calls += [lambda: moe.grouped_linear(_Huge(5, 16), _Huge(W + 2, 24, 16), _Huge(W + 3, dtype=torch.int32))]
+    for n, f in ((W + 5, 16), (5, W + 16)):
+        calls += [lambda n=n, f=f: moe.swiglu(_Huge(n, 2 * f)),
+                  lambda n=n, f=f: moe.swiglu_backward(_Huge(n, f), _Huge(n, 2 * f))]
+    for call in calls:
+        with pytest.raises(moe.MoEError) as e:
+            call()
+        assert e.value.status == S.UNSUPPORTED_SHAPE
