@@ -152,19 +152,18 @@ class _Huge:
     """What the functions ask of a CUDA tensor, with any shape and no memory behind it."""
 
     is_cuda = True
-    device = torch.device("cuda", 0)
 
-    def __init__(self, *shape, dtype=torch.bfloat16):
-        self.shape, self.dtype = torch.Size(shape), dtype
+    def __init__(self, *shape, dtype=torch.bfloat16, index=0, contiguous=True):
+        self.shape, self.dtype, self.device, self.contiguous = torch.Size(shape), dtype, torch.device("cuda", index), contiguous
 
     def dim(self):
         return len(self.shape)
 
     def get_device(self):
-        return 0
+        return self.device.index
 
     def is_contiguous(self):
-        return True
+        return self.contiguous
 
     def data_ptr(self):
         return A[0]
@@ -194,3 +193,63 @@ def test_sizes_that_do_not_fit_the_abi(lib, monkeypatch):
         with pytest.raises(moe.MoEError) as e:
             call()
         assert e.value.status == S.UNSUPPORTED_SHAPE
+
+
+def test_python_refuses_tensors_that_do_not_fit(lib, monkeypatch):
+    """Every argument of every function: a wrong shape, type, device or layout, before the library is called."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(moe.linear_ops, "lib", lambda: pytest.fail("the library was called"))
+    T, K, N, E, bf = 4, 16, 24, 3, torch.bfloat16
+    good = {
+        moe.linear: dict(x=(T, K), w=(N, K), bias=(N,), residual=(T, N), out=(T, N)),
+        moe.linear_backward: dict(dy=(T, N), x=(T, K), w=(N, K), preact=(T, N)),
+        moe.grouped_linear: dict(x=(T, K), w=(E, N, K), offsets=(E + 1,), out=(T, N)),
+        moe.grouped_linear_backward: dict(dy=(T, N), x=(T, K), w=(E, N, K), offsets=(E + 1,), dx=(T, K)),
+        moe.swiglu: dict(gu=(T, 2 * K), out=(T, K)),
+        moe.swiglu_backward: dict(dh=(T, K), gu=(T, 2 * K), out=(T, 2 * K)),
+    }
+    for fn, shapes in good.items():
+        more = dict(activation=moe.ACT_SILU) if fn is moe.linear_backward else {}
+        for name, shape in shapes.items():
+            dtype = torch.int32 if name == "offsets" else bf
+            longer = (shape[0],) * (len(shape) == 2) + (shape[-1] + 8,) if name != "gu" else (shape[0], shape[1] + 1)
+            for bad in (_Huge(*longer, dtype=dtype), _Huge(*shape, dtype=torch.float16), _Huge(*shape, 1, dtype=dtype),
+                        _Huge(*shape, dtype=torch.int64 if name == "offsets" else torch.float32),
+                        _Huge(*shape, dtype=dtype, contiguous=False)):
+                args = {k: _Huge(*v, dtype=torch.int32 if k == "offsets" else bf) for k, v in shapes.items()}
+                args[name] = bad
+                with pytest.raises(ValueError):
+                    fn(**args, **more)
+            if name != next(iter(shapes)) and not (name in ("x", "gu") and "dy" in shapes or "dh" in shapes):
+                args = {k: _Huge(*v, dtype=torch.int32 if k == "offsets" else bf) for k, v in shapes.items()}
+                args[name] = _Huge(*shape, dtype=dtype, index=1)
+                with pytest.raises(ValueError, match="cuda:1"):
+                    fn(**args, **more)
+
+
+def test_python_refuses_other_arguments(lib, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    x, w, dy, off = _Huge(4, 16), _Huge(24, 16), _Huge(4, 24), _Huge(2, dtype=torch.int32)
+    we = _Huge(1, 24, 16)
+    with pytest.raises(ValueError, match="preact"):
+        moe.linear_backward(dy, x, w, activation=moe.ACT_GELU)
+    for call in (lambda t: moe.linear_backward(dy, x, w, grad_dtype=t), lambda t: moe.grouped_linear(x, we, off, out_dtype=t),
+                 lambda t: moe.grouped_linear_backward(dy, x, we, off, grad_dtype=t)):
+        with pytest.raises(ValueError, match="output type"):
+            call(torch.float16)
+
+    class Stream:
+        device = torch.device("cuda", 1)
+        cuda_stream = 0
+
+    for call in (lambda: moe.linear(x, w, stream=Stream()), lambda: moe.linear_backward(dy, x, w, stream=Stream()),
+                 lambda: moe.grouped_linear(x, we, off, stream=Stream()), lambda: moe.swiglu(x, stream=Stream()),
+                 lambda: moe.grouped_linear_backward(dy, x, we, off, stream=Stream()),
+                 lambda: moe.swiglu_backward(_Huge(4, 8), x, stream=Stream())):
+        with pytest.raises(ValueError, match="the stream belongs to cuda:1"):
+            call()
+    for bad in (-1, 4):
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+        with pytest.raises(moe.MoEError) as e:
+            moe.linear(x, w, activation=bad)
+        assert e.value.status == S.INVALID_ARG
