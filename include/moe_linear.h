@@ -39,6 +39,13 @@ typedef enum {
     MOE_ACT_SILU = 2,   /* z / (1 + exp(-z)) */
     MOE_ACT_GELU = 3    /* z Phi(z), Phi the normal distribution function (the exact form) */
 } moe_activation;
+/*
+ * Before the one rounding, values and slopes are off by less than 2^-20 (1 + |z|)
+ * and, where z < -2, by less than 2^-9 of themselves (SiLU: 2^-16); what a factor
+ * below 2^-126 makes is 0.  Infinite z: GELU and its slope take their limits;
+ * SiLU (and SwiGLU) follow the formula in IEEE arithmetic, which gives NaN at
+ * minus infinity and for the slope at both.
+ */
 
 /*
  * moe_linear_forward:
@@ -60,7 +67,10 @@ MOE_API moe_status moe_linear_forward(const void* x, int32_t T, int32_t K, const
  * moe_linear_backward -- the gradients of moe_linear_forward:
  *   dz = dy * act'(preact);  dx = dz W;  dw = dz^T x;  dbias = sum_t dz[t]
  * (the residual's gradient is dy itself).  dz is computed in fp32; dbias sums
- * it unrounded, the products take it rounded to bf16.
+ * it unrounded, the products take it rounded to bf16: the tensor cores' operands
+ * are bf16, and dz as a sum of two of them would double the operations.  With
+ * normal inputs and GELU, dx and bf16 dw are then off by 2.3e-3 of their norms
+ * (1.7e-3 from their own rounding), fp32 dw by 1.7e-3.
  *   dy  bf16 [T, N];  x  bf16 [T, K];  w  bf16 [N, K]
  *   preact  bf16 [T, N] as moe_linear_forward wrote it; not read when
  *           activation is MOE_ACT_NONE (NULL is fine there)

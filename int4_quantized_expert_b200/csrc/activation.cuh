@@ -48,8 +48,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// 1 / (1 + exp(-z)): a few ulps of fp32.  For z below about -88 the power of two
-// is infinite and the result 0.
+// 1 / (1 + exp(-z)), off by less than 2^-17 of itself: the power of two's exponent
+// is rounded to fp32, by 2^-18 at |z| = 88 and 2^-21 at 8.  Below 2^-126 (z < -87.3)
+// the result is 0.
 __device__ __forceinline__ float sigmoid_fast(float z) { return rcp_ftz(1.0f + ex2_ftz(-1.44269504f * z)); }
 
 // h = Phi(-|z|), the normal distribution function, as 2^(-z^2 / (2 ln 2) + Q(|z|)):

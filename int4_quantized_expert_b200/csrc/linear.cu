@@ -802,6 +802,9 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
 // ---------------------------------------------------------------------------
 // dz = dy * act'(z) and dbias = sum over the rows of dz (unrounded)
 //
+// dz is rounded to bf16 for the products that read it, whose operands are bf16
+// (dy of a layer without activation has that type too); dbias takes it before.
+//
 // HBM-bound: dy and z are read once, dz is written once, the column sums ride
 // along.  A cluster of AG_SPLIT CTAs takes a strip of AG_COLS columns: 8 threads
 // x 16 bytes a row (one 128-byte line), 32 rows at a time, each CTA a part of

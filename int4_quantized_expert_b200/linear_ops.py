@@ -7,7 +7,10 @@ As in the rest of the package, the functions only check and marshal arguments
 into the C ABI (``include/moe_linear.h``).  They run on the device of their
 tensors, on ``stream`` or that device's current stream, and allocate what they
 return (and nothing else, except ``linear_backward``'s dz) on that stream.
-``linear_device_status`` reports what the kernels found wrong.
+As everywhere in the package, what a call reads has to stay allocated until the
+stream is past it, and autograd does not record the calls: the ``*_backward``
+functions are the gradients.  ``linear_device_status`` reports what the kernels
+found wrong.
 """
 from __future__ import annotations
 

@@ -169,3 +169,17 @@ def test_gelu_of_infinite_values():
                    torch.cat([z, torch.zeros(3).bfloat16()]).cuda(), activation=moe.ACT_GELU)
     assert y[:, 0].eq(inf).all() and y[:, 1].eq(0).all() and y[:, 2].isnan().all()
     assert y[:, 3].eq(z[3].item()).all() and y[:, 4].eq(0).all()
+
+
+def test_silu_everywhere():
+    """The sigmoid is off by less than 2^-17 of itself (its exponent's rounding, 2^-18 at 88, the hardware's power
+    and reciprocal); the slope s (1 + z (1 - s)) adds the roundings of a sum that is not below 1/2 for z < -2.
+    Where the sigmoid is below 2^-126 it is 0."""
+    z = every_bf16(2.0 ** -20, 100.0)
+    fz = f64(z)
+    got, want = f64(through_activation(z, moe.ACT_SILU)), ol.act(fz, "silu")
+    assert (np.abs(got - want) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(want) + 2.0 ** -119).all()
+    got, want = f64(through_slope(z, moe.ACT_SILU)), ol.act_slope(fz, "silu")
+    assert (np.abs(got - want) <= 2.0 ** -20 * (1 + np.abs(fz))).all()
+    tail = fz < -2
+    assert (np.abs(got - want) <= 2.0 ** -16 * np.abs(want) + 2.0 ** -119)[tail].all()
