@@ -396,34 +396,24 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
     if (p.offsets) griddep_wait();
 
     // the row ranges, and for LIN_FWD / LIN_DX the chunks before each expert
-    int chunks = 0, begin = 0, count = 0;
+    int chunks = 0;
+    bool bad = false;
     if (int(threadIdx.x) < p.E) {
-        count = p.rows;
+        int b = 0, c = p.rows;
         if (p.offsets) {
-            begin = p.offsets[threadIdx.x];
+            b = p.offsets[threadIdx.x];
             const int end = p.offsets[threadIdx.x + 1];
-            count = in_order(begin, end, p.rows) ? end - begin : -1;
-        }
-    }
-    // Where two offsets are out of order, ranges that are in order by themselves may
-    // overlap.  Those that overlap an earlier one count as empty too: a grid of split
-    // tiles has room for the chunks of ranges that are apart and no more.
-    if (p.offsets && __syncthreads_or(count < 0)) {
-        if (int(threadIdx.x) < p.E) {
-            for (int i = 0; count > 0 && i < int(threadIdx.x); ++i) {
-                const int b = p.offsets[i], end = p.offsets[i + 1];
-                if (in_order(b, end, p.rows) && max(b, begin) < min(end, begin + count)) count = -1;
-            }
-            if (count < 0) {
-                begin = count = 0;
+            if (in_order(b, end, p.rows)) {
+                c = end - b;
+            } else {
+                b = c = 0;
+                bad = true;
                 if (blockIdx.x == 0) atomicOr(&g_linear_status, DEV_BAD_EXPERT);
             }
         }
-    }
-    if (int(threadIdx.x) < p.E) {
-        sm->begin[threadIdx.x] = begin;
-        sm->count[threadIdx.x] = count;
-        chunks = p.offsets ? row_chunks(count, p.bn) : p.chunks;
+        sm->begin[threadIdx.x] = b;
+        sm->count[threadIdx.x] = c;
+        chunks = p.offsets ? row_chunks(c, p.bn) : p.chunks;
     }
     if (MODE != LIN_DW) {
         int incl = chunks;
@@ -442,7 +432,27 @@ __global__ void __launch_bounds__(LN_THREADS, SHARE == LIN_SPLIT ? 2 : 1) linear
         }
     }
     tc_fence_before();
-    __syncthreads();
+    // Where two offsets are out of order, ranges that are in order by themselves may
+    // overlap.  Those that overlap an earlier one count as empty too: a grid of split
+    // tiles has room for the chunks of ranges that are apart and no more.
+    if (__syncthreads_or(bad)) {
+        if (int(threadIdx.x) < p.E) {
+            const int b = sm->begin[threadIdx.x], end = b + sm->count[threadIdx.x];
+            bool overlaps = false;
+            for (int i = 0; i < int(threadIdx.x) && !overlaps; ++i) {
+                const int bi = p.offsets[i], ei = p.offsets[i + 1];
+                overlaps = in_order(bi, ei, p.rows) && max(b, bi) < min(end, ei);
+            }
+            if (overlaps) {
+                sm->count[threadIdx.x] = 0;
+                if (blockIdx.x == 0) atomicOr(&g_linear_status, DEV_BAD_EXPERT);
+            }
+        }
+        __syncthreads();
+        if (MODE != LIN_DW && threadIdx.x == 0)
+            for (int e = 0; e < p.E; ++e) sm->first[e + 1] = sm->first[e] + row_chunks(sm->count[e], p.bn);
+        __syncthreads();
+    }
     // the other CTAs' barriers are initialized (a pair's allocations done)
     if (PAIR || (SPLIT && p.split > 1)) cluster_sync();
     tc_fence_after();
