@@ -183,3 +183,73 @@ def test_silu_everywhere():
     assert (np.abs(got - want) <= 2.0 ** -20 * (1 + np.abs(fz))).all()
     tail = fz < -2
     assert (np.abs(got - want) <= 2.0 ** -16 * np.abs(want) + 2.0 ** -119)[tail].all()
+
+
+# ---------------------------------------------------------------------------
+# the largest grouped calls
+# ---------------------------------------------------------------------------
+def normal(seed, *shape, std=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.empty(*shape, dtype=torch.bfloat16, device="cuda").normal_(0.0, std, generator=g)
+
+
+def test_grouped_weights_past_32_bits():
+    """256 experts with 2^33 weights in all, the last experts' rows past 2^32 values."""
+    E, K, N = 256, 4096, 8192
+    counts = torch.zeros(E, dtype=torch.int64)
+    counts[[0, 127, 128, 200, 255]] = torch.tensor([3, 70, 1, 300, 17])
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), counts.cumsum(0)])
+    n = int(off[-1])
+    x, w, dy = normal(1, n, K), normal(2, E, N, K, std=K ** -0.5), normal(3, n, N)
+    y = moe.grouped_linear(x, w, off.int().cuda())
+    dx, dw = moe.grouped_linear_backward(dy, x, w, off.int().cuda())
+    assert moe.linear_device_status() == moe.Status.OK
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        if s.start == s.stop:
+            assert not dw[e].any()
+            continue
+        X, W, D = f64(x[s]), f64(w[e]), f64(dy[s])
+        check(y[s], X @ W.T, sum_tol(K, np.abs(X) @ np.abs(W).T))
+        check(dx[s], D @ W, sum_tol(N, np.abs(D) @ np.abs(W)))
+        check(dw[e], D.T @ X, sum_tol(len(X), np.abs(D).T @ np.abs(X)))
+
+
+@pytest.mark.parametrize("counts", [[1 << 20], [0, (1 << 20) - 7, 7, 0], [(1 << 20) // 256] * 256])
+def test_grouped_most_rows(counts):
+    n, E, K, N = sum(counts), len(counts), 24, 40
+    off = np.concatenate([[0], np.cumsum(counts)])
+    x, w, dy = normal(4, n, K), normal(5, E, N, K), normal(6, n, N)
+    oc = torch.from_numpy(off).int().cuda()
+    y = moe.grouped_linear(x, w, oc, out_dtype=torch.float32)
+    dx, dw = moe.grouped_linear_backward(dy, x, w, oc, grad_dtype=torch.float32)
+    assert moe.linear_device_status() == moe.Status.OK
+    fx, fw, fdy = f64(x), f64(w), f64(dy)
+    (rdx, rdw), (Sdx, Sdw) = ol.grouped_backward(fdy, fx, fw, off), ol.grouped_backward(abs(fdy), abs(fx), abs(fw), off)
+    check(y, ol.grouped(fx, fw, off), sum_tol(K, ol.grouped(abs(fx), abs(fw), off)))
+    check(dx, rdx, sum_tol(N, Sdx))
+    check(dw, rdw, sum_tol(max(counts), Sdw))
+
+
+# ---------------------------------------------------------------------------
+# beside other work
+# ---------------------------------------------------------------------------
+def test_beside_products_on_another_stream():
+    """Single tiles, pairs and split tiles on one stream, torch's products on another, at the same time: the same
+    results as alone."""
+    shapes = [(1, 4096, 4096), (40, 2048, 1024), (300, 1032, 2056), (3000, 520, 2056), (64, 256, 512)]
+    args = [(normal(i, T, K), normal(i + 9, N, K, std=K ** -0.5)) for i, (T, K, N) in enumerate(shapes)]
+    a, b = normal(30, 2048, 2048), normal(31, 2048, 2048)
+    want, prod = [moe.linear(*v) for v in args], a @ b
+    torch.cuda.synchronize()
+    mine, other = torch.cuda.Stream(), torch.cuda.Stream()
+    got, prods = [], []
+    for _ in range(30):
+        got.append([moe.linear(*v, stream=mine) for v in args])
+        with torch.cuda.stream(other):
+            prods.append(a @ b)
+            prods.append(a[:64] @ b)
+    torch.cuda.synchronize()
+    assert moe.linear_device_status() == moe.Status.OK
+    assert all(torch.equal(g, w) for row in got for g, w in zip(row, want))
+    assert all(torch.equal(p, prod) for p in prods[::2])
