@@ -1195,9 +1195,12 @@ moe_status linear_device_status(cudaStream_t stream) {
     static std::mutex mu;   // g_linear_taken belongs to one query at a time
     if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;   // not under the lock
     std::lock_guard<std::mutex> lock(mu);
-    take_status_kernel<<<1, 1, 0, stream>>>();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = cfg.blockDim = dim3(1);
+    cfg.stream = stream;
     int32_t v = 0;
-    if (launch_status() != MOE_OK ||
+    // this launch's own result: an error that some call before left behind must not cost a report
+    if (cudaLaunchKernelEx(&cfg, take_status_kernel) != cudaSuccess ||
         cudaMemcpyFromSymbolAsync(&v, g_linear_taken, sizeof(v), 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
         cudaStreamSynchronize(stream) != cudaSuccess)
         return MOE_ERR_CUDA;

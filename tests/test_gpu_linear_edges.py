@@ -1,6 +1,9 @@
 """The linear, grouped and SwiGLU operators where callers or values go astray:
 offsets out of order, reports from several streams, the activations' far ends.
 Tolerances as derived in test_gpu_linear.py."""
+import os
+import subprocess
+import sys
 import threading
 
 import numpy as np
@@ -253,3 +256,27 @@ def test_beside_products_on_another_stream():
     assert moe.linear_device_status() == moe.Status.OK
     assert all(torch.equal(g, w) for row in got for g, w in zip(row, want))
     assert all(torch.equal(p, prod) for p in prods[::2])
+
+
+def test_report_survives_an_error_of_another_call():
+    """A query that fails because its stream is being captured leaves an error behind in this thread; the
+    next query returns the report all the same."""
+    code = """
+import torch, int4_quantized_expert_b200 as moe
+x, w = torch.zeros(64, 32).bfloat16().cuda(), torch.zeros(2, 48, 32).bfloat16().cuda()
+bad = torch.tensor([0, 20, 65], dtype=torch.int32, device="cuda")
+assert moe.linear_device_status() == moe.Status.OK
+moe.grouped_linear(x, w, bad)
+torch.cuda.synchronize()
+g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.stream(s):
+    g.capture_begin()
+    assert moe.linear_device_status(s) == moe.Status.CUDA
+    try:
+        g.capture_end()
+    except RuntimeError:
+        pass
+assert moe.linear_device_status() == moe.Status.INVALID_ARG
+assert moe.linear_device_status() == moe.Status.OK
+"""
+    subprocess.run([sys.executable, "-c", code], check=True, timeout=300, cwd=os.path.dirname(os.path.dirname(__file__)))
