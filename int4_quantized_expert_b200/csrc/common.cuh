@@ -43,25 +43,50 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Kernels whose attributes are set already, by device.  Without memory for an entry
+// they are set again in the next call: nothing is thrown through the C entry points.
+class KernelsDone {
+    std::mutex mu;
+    std::set<std::pair<const void*, int>> done;
+
+public:
+    template <typename Set>
+    moe_status once(const void* kernel, Set set) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(mu);
+        if (done.count({kernel, dev})) return MOE_OK;
+        if (!set(dev)) return MOE_ERR_CUDA;
+        try {
+            done.insert({kernel, dev});
+        } catch (...) {
+        }
+        return MOE_OK;
+    }
+};
+
 // Allow a kernel the device's largest dynamic shared memory, once per device.
 template <typename... KArgs>
 inline moe_status allow_max_smem(void (*kernel)(KArgs...)) {
-    static std::mutex mu;
-    static std::set<std::pair<const void*, int>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
-    if (done.count(key)) return MOE_OK;
-    int optin = 0;
-    cudaFuncAttributes fa;
-    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-        cudaFuncGetAttributes(&fa, kernel) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             optin - int(fa.sharedSizeBytes)) != cudaSuccess)   // static shared memory counts too
-        return MOE_ERR_CUDA;
-    done.insert(key);
-    return MOE_OK;
+    static KernelsDone done;
+    return done.once(reinterpret_cast<const void*>(kernel), [&](int dev) {
+        int optin = 0;
+        cudaFuncAttributes fa;
+        return cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) == cudaSuccess &&
+               cudaFuncGetAttributes(&fa, kernel) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    optin - int(fa.sharedSizeBytes)) == cudaSuccess;   // static shared memory counts too
+    });
+}
+
+// As much shared memory on an SM as two blocks of a kernel need, once per device.
+template <typename... KArgs>
+inline moe_status prefer_smem(void (*kernel)(KArgs...)) {
+    static KernelsDone done;
+    return done.once(reinterpret_cast<const void*>(kernel), [&](int) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                    cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+    });
 }
 
 template <typename... KArgs, typename... Args>

@@ -939,23 +939,6 @@ moe_status launch_cluster(void (*kernel)(KArgs...), unsigned grid, unsigned bloc
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
 }
 
-// As much shared memory as two blocks need, once per device (see allow_max_smem).
-template <typename... KArgs>
-moe_status prefer_smem(void (*kernel)(KArgs...)) {
-    static std::mutex mu;
-    static std::set<std::pair<const void*, int>> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return MOE_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_pair(reinterpret_cast<const void*>(kernel), dev);
-    if (done.count(key)) return MOE_OK;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
-    done.insert(key);
-    return MOE_OK;
-}
-
 // Chunks of all rows for pairs: the fewest that take the least time, counted as
 // rounds of tiles over the pairs times the cycles of a step, which are those of
 // the MMAs (2 a column) or of the loads (128 rows of A and half of the columns,
